@@ -172,7 +172,7 @@ def prepare(case, seed):
         else:
             st["cache"] = bsva.PagedKVCache.over(st["pk"], st["pv"], st.get("sk"), st.get("sv"))
             st["batch"] = bsva.PagedBatch(st["q_start"], st["kv_len"], st["table"], st["max_q"], st["max_kv"])
-            st["ws"] = st["cache"].new_workspace(st["batch"], case.get("Hq", case["Hkv"]))
+            st["ws"] = st["cache"].new_workspace(st["batch"], case.get("Hq", case["Hkv"]), st["q" if "q" in st else "k"].shape[0])
     return st
 
 
