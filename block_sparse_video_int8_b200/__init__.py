@@ -20,6 +20,11 @@ Entry points (same names as the C ABI):
 * ``KVCache(B, H, d, n_slots)``              the INT8 streaming K/V cache in 128-row slabs:
   ``append(k, v)`` (``bsva_kv_cache_append``) and ``attend(qq, mask)``
   (``masked_block_attn_fwd_kvcache``)
+* ``PagedKVCache(n_pages, page_size, H, d)`` a paged K/V cache for causal generation, INT8 per token
+  and head or bf16: ``write(k, v, batch)`` (``bsva_paged_kv_write``), ``read(batch)``
+  (``bsva_paged_kv_read``) and ``attend(q, batch)`` (``paged_attn_fwd``); the sequences of a call
+  are a ``PagedBatch``
+* ``cross_attn_fwd(q, k, v, k_len)``         attention to an encoder's states of another length
 """
 from __future__ import annotations
 
@@ -35,7 +40,7 @@ __all__ = [
     "sparse_attn_route_topk", "build_lcsa_mask", "quantize_v", "masked_block_attn_fwd_v8", "sparse_attn_fwd",
     "masked_block_attn_fwd", "check_status", "selftest_timeout", "new_workspace",
     "build_centroids", "sparse_attn_core", "virtual_kv_workspace_bytes", "virtual_kv_residual_fwd",
-    "quantize_q", "KVCache",
+    "quantize_q", "KVCache", "PagedBatch", "PagedKVCache", "cross_attn_fwd", "new_cross_attn_workspace",
 ]
 
 ABI_VERSION = 5
@@ -65,6 +70,20 @@ class KVCacheStruct(ctypes.Structure):
                 ("k8", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v8", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("slab_rows", ctypes.c_void_p),
                 ("first", ctypes.c_int), ("count", ctypes.c_int)]
+
+
+class PagedKVStruct(ctypes.Structure):
+    """``bsva_paged_kv``."""
+    _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class PagedBatchStruct(ctypes.Structure):
+    """``bsva_paged_batch``."""
+    _fields_ = [("S", ctypes.c_int), ("T", ctypes.c_int), ("max_q", ctypes.c_int), ("max_kv", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
 
 
 def lib_path() -> str:
@@ -114,6 +133,18 @@ _SIGS = {
     "virtual_kv_residual_fwd": (ctypes.c_int, [Shape, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P,
                                                ctypes.POINTER(ctypes.c_int), ctypes.c_int, ctypes.c_int,
                                                ctypes.c_float, ctypes.c_int, _P, _P, _P, ctypes.c_size_t, _P]),
+    "bsva_paged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedBatchStruct),
+                                                     ctypes.c_int]),
+    "bsva_paged_kv_write": (ctypes.c_int, [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedBatchStruct), _P, _P,
+                                           ctypes.c_longlong, ctypes.c_longlong, _P, ctypes.c_size_t, _P]),
+    "bsva_paged_kv_read": (ctypes.c_int, [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedBatchStruct), _P,
+                                          ctypes.c_int, _P, _P, _P, ctypes.c_size_t, _P]),
+    "paged_attn_fwd": (ctypes.c_int, [ctypes.POINTER(PagedKVStruct), ctypes.POINTER(PagedBatchStruct), _P,
+                                      ctypes.c_longlong, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
+                                      _P, _P, _P, ctypes.c_size_t, _P]),
+    "bsva_cross_attn_workspace_bytes": (ctypes.c_size_t, [Shape, ctypes.c_int]),
+    "cross_attn_fwd": (ctypes.c_int, [Shape, ctypes.c_int, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
 }
 
 
@@ -583,3 +614,231 @@ class KVCache:
                                                     OUT_DTYPES[out.dtype], _ptr(out), _ptr(lse), _ptr(workspace),
                                                     workspace.numel(), _stream(stream)))
         return (out, lse) if with_lse else out
+
+
+# ------------------------------------------------------------------------- paged K/V cache, cross attention
+def _on(device, name, *tensors):
+    """The tensors of a call lie on one CUDA device (the library works on the current one)."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+
+
+def _token_stride(t, H, d, name):
+    """Elements between the tokens of [T, H, d] whose heads and values are dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dim() != 3 or t.shape[2] != d or (H is not None and t.shape[1] != H):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, {H or 'heads'}, {d}]")
+    H = t.shape[1]
+    if t.shape[0] <= 1:
+        if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        return H * d
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d) or t.stride(0) < H * d or t.stride(0) % 8:
+        raise ValueError(f"{name}: strides {t.stride()}; the heads of a token must be contiguous and tokens a multiple "
+                         "of 8 elements apart, at least heads * d")
+    return t.stride(0)
+
+
+class PagedBatch:
+    """The sequences of a call on a ``PagedKVCache`` (C ABI ``bsva_paged_batch``).
+
+    ``q_start`` int32 [S+1]: sequence s has new tokens ``q_start[s] .. q_start[s+1]-1`` of the packed tensors;
+    ``kv_len`` int32 [S]: its tokens, the new ones included; ``page_table`` int32 [S, max_pages]. ``max_q`` and
+    ``max_kv`` are host bounds of new tokens and tokens of a sequence. The tensors are kept and read by every
+    call, so a captured graph replays with what they hold then."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_q: int, max_kv: int):
+        _need(kv_len, torch.int32, None, "kv_len")
+        if kv_len.dim() != 1 or kv_len.shape[0] < 1:
+            raise ValueError(f"kv_len has shape {tuple(kv_len.shape)}, expected [S]")
+        S = kv_len.shape[0]
+        _need(q_start, torch.int32, (S + 1,), "q_start")
+        _need(page_table, torch.int32, None, "page_table")
+        if page_table.dim() != 2 or page_table.shape[0] != S:
+            raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{S}, max_pages]")
+        _on(kv_len.device, "q_start", q_start)
+        _on(kv_len.device, "page_table", page_table)
+        self.S, self.max_q, self.max_kv = S, int(max_q), int(max_kv)
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.device = kv_len.device
+
+    def _struct(self, T: int) -> PagedBatchStruct:
+        return PagedBatchStruct(self.S, T, self.max_q, self.max_kv, self.page_table.shape[1], self.q_start.data_ptr(),
+                                self.kv_len.data_ptr(), self.page_table.data_ptr())
+
+
+class PagedKVCache:
+    """A paged K/V cache (C ABI ``bsva_paged_kv``): pages [n_pages, H, page_size, d] of INT8 codes with an fp32
+    scale for each (token, head), or of bf16 values (``dtype=torch.bfloat16``).
+
+    ``workspace`` of the calls is a zeroed device uint8 buffer of ``new_workspace`` (its status word is read by
+    ``check_status``); without one, each call allocates its own. Calls that may run at the same time need one each."""
+
+    def __init__(self, n_pages: int, page_size: int, H: int, d: int, dtype=torch.int8, device=None):
+        if dtype not in (torch.int8, torch.bfloat16):
+            raise TypeError(f"dtype must be torch.int8 or torch.bfloat16, got {dtype}")
+        dev = device or "cuda"
+        shape = (n_pages, H, page_size, d)
+        k, v = (torch.zeros(shape, dtype=dtype, device=dev) for _ in range(2))
+        ks, vs = ((torch.zeros(shape[:3], dtype=torch.float32, device=dev) for _ in range(2))
+                  if dtype == torch.int8 else (None, None))
+        self._init(k, v, ks, vs)
+
+    @classmethod
+    def over(cls, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+             v_scale: torch.Tensor | None = None) -> "PagedKVCache":
+        """A cache over existing buffers: int8 pages with their scales, or bf16 pages."""
+        self = cls.__new__(cls)
+        self._init(k, v, k_scale, v_scale)
+        return self
+
+    def _init(self, k, v, ks, vs):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.dtype not in (torch.int8, torch.bfloat16):
+            raise TypeError("k must be an int8 or bf16 tensor [n_pages, H, page_size, d]")
+        _need(k, k.dtype, None, "k")
+        _need(v, k.dtype, tuple(k.shape), "v")
+        if k.dtype == torch.int8:
+            _need(ks, torch.float32, tuple(k.shape[:3]), "k_scale")
+            _need(vs, torch.float32, tuple(k.shape[:3]), "v_scale")
+        elif ks is not None or vs is not None:
+            raise ValueError("bf16 pages have no scales")
+        for n, t in (("v", v), ("k_scale", ks), ("v_scale", vs)):
+            _on(k.device, n, t)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, ks, vs
+        self.n_pages, self.H, self.page_size, self.d = k.shape
+        self.c = PagedKVStruct(self.n_pages, self.page_size, self.H, self.d, 0 if k.dtype == torch.int8 else 1,
+                               k.data_ptr(), v.data_ptr(), ks.data_ptr() if ks is not None else None,
+                               vs.data_ptr() if vs is not None else None)
+
+    def workspace_bytes(self, batch: PagedBatch, Hq: int, T: int | None = None) -> int:
+        """Bytes for calls of ``T`` packed rows (by default S * max_q) and up to ``Hq`` query heads."""
+        b = batch._struct(batch.S * batch.max_q if T is None else T)
+        n = load().bsva_paged_workspace_bytes(ctypes.byref(self.c), ctypes.byref(b), Hq)
+        if n == 0:
+            raise BsvaError(1, load().bsva_last_error().decode(errors="replace"))
+        return n
+
+    def new_workspace(self, batch: PagedBatch, Hq: int, T: int | None = None) -> torch.Tensor:
+        return torch.zeros(self.workspace_bytes(batch, Hq, T), dtype=torch.uint8, device=self.k.device)
+
+    def _workspace(self, workspace, need):
+        if workspace is None:
+            return torch.zeros(need, dtype=torch.uint8, device=self.k.device)
+        _need(workspace, torch.uint8, None, "workspace")
+        _on(self.k.device, "workspace", workspace)
+        return workspace
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, batch: PagedBatch, workspace=None, stream=None):
+        """The batch's new tokens, bf16 [T, H, d], into their pages (C ABI ``bsva_paged_kv_write``); tokens may be
+        strided, as slices of a fused projection are."""
+        ks, vs = _token_stride(k, self.H, self.d, "k"), _token_stride(v, self.H, self.d, "v")
+        if v.shape[0] != k.shape[0]:
+            raise ValueError(f"k has {k.shape[0]} tokens, v has {v.shape[0]}")
+        for n, t in (("k", k), ("v", v), ("batch", batch)):
+            _on(self.k.device, n, t)
+        with torch.cuda.device(self.k.device):
+            ws = self._workspace(workspace, 256)
+            b = batch._struct(k.shape[0])
+            _check(load().bsva_paged_kv_write(ctypes.byref(self.c), ctypes.byref(b), _ptr(k), _ptr(v), ks, vs, _ptr(ws),
+                                              ws.numel(), _stream(stream)))
+
+    def read(self, batch: PagedBatch, first: torch.Tensor | None = None, length: int | None = None, out=None,
+             workspace=None, stream=None):
+        """Cached tokens ``first[s]`` (default 0) to the end of each sequence as bf16 (k, v) [S, H, length, d], zeros
+        behind them; ``length`` defaults to ``max_kv`` (C ABI ``bsva_paged_kv_read``)."""
+        L = batch.max_kv if length is None else int(length)
+        if first is not None:
+            _need(first, torch.int32, (batch.S,), "first")
+        shape = (batch.S, self.H, L, self.d)
+        for n, t in (("first", first), ("batch", batch)):
+            _on(self.k.device, n, t)
+        with torch.cuda.device(self.k.device):
+            if out is None:
+                out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=self.k.device) for _ in range(2))
+            for n, t in (("k_out", out[0]), ("v_out", out[1])):
+                _need(t, torch.bfloat16, shape, n)
+                _on(self.k.device, n, t)
+            ws = self._workspace(workspace, 256)
+            b = batch._struct(0)
+            _check(load().bsva_paged_kv_read(ctypes.byref(self.c), ctypes.byref(b), _ptr(first), L, _ptr(out[0]),
+                                             _ptr(out[1]), _ptr(ws), ws.numel(), _stream(stream)))
+        return out
+
+    def attend(self, q: torch.Tensor, batch: PagedBatch, causal: bool = True, window: int = 0,
+               softmax_scale: float = 0.0, with_lse: bool = False, workspace=None, out=None, lse=None, stream=None):
+        """Attention of the batch's new tokens, q bf16 [T, Hq, d], over their sequences' cached keys (C ABI
+        ``paged_attn_fwd``). Returns ``out`` [T, Hq, d] or ``(out, lse)``; rows behind the last sequence are left as
+        they were (``out`` and ``lse`` that the call allocates: zeros)."""
+        qs = _token_stride(q, None, self.d, "q")
+        T, Hq, d = q.shape
+        for n, t in (("q", q), ("batch", batch)):
+            _on(self.k.device, n, t)
+        with torch.cuda.device(self.k.device):
+            if out is None:
+                out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+            if with_lse and lse is None:
+                lse = torch.zeros((T, Hq), dtype=torch.float32, device=q.device)
+            _need(out, torch.bfloat16, (T, Hq, d), "out")
+            _on(self.k.device, "out", out)
+            if lse is not None:
+                _need(lse, torch.float32, (T, Hq), "lse")
+                _on(self.k.device, "lse", lse)
+            b = batch._struct(T)
+            ws = workspace
+            if ws is None:
+                need = load().bsva_paged_workspace_bytes(ctypes.byref(self.c), ctypes.byref(b), Hq)
+                ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+            ws = self._workspace(ws, 0)
+            _check(load().paged_attn_fwd(ctypes.byref(self.c), ctypes.byref(b), _ptr(q), qs, Hq, int(causal), int(window),
+                                         ctypes.c_float(softmax_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                         _stream(stream)))
+        return (out, lse) if with_lse else out
+
+
+def _cross_shape(q, k):
+    for n, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{n} must be a tensor [B, heads, length, d]")
+    B, Hq, Lq, d = q.shape
+    return Shape(B, Hq, Lq, k.shape[2], d, 0), k.shape[1]
+
+
+def new_cross_attn_workspace(q: torch.Tensor, k: torch.Tensor) -> torch.Tensor:
+    """A zeroed workspace for ``cross_attn_fwd`` on tensors of these shapes."""
+    s, Hkv = _cross_shape(q, k)
+    n = load().bsva_cross_attn_workspace_bytes(s, Hkv)
+    if n == 0:
+        raise BsvaError(1, load().bsva_last_error().decode(errors="replace"))
+    return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_len: torch.Tensor | None = None,
+                   softmax_scale: float = 0.0, with_lse: bool = False, workspace=None, out=None, lse=None, stream=None):
+    """Attention of q bf16 [B, H, Lq, d] to k, v bf16 [B, Hkv, Lk, d], the first ``k_len[b]`` (int32 [B], default Lk)
+    keys of each batch entry (C ABI ``cross_attn_fwd``). H is a multiple of Hkv."""
+    s, Hkv = _cross_shape(q, k)
+    _need(q, torch.bfloat16, None, "q")
+    _need(k, torch.bfloat16, (s.B, Hkv, s.Lk, s.d), "k")
+    _need(v, torch.bfloat16, (s.B, Hkv, s.Lk, s.d), "v")
+    if k_len is not None:
+        _need(k_len, torch.int32, (s.B,), "k_len")
+    with torch.cuda.device(q.device):
+        out = _out(out, (s.B, s.H, s.Lq, s.d), torch.bfloat16, q.device)
+        if with_lse and lse is None:
+            lse = torch.empty((s.B, s.H, s.Lq), dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _need(lse, torch.float32, (s.B, s.H, s.Lq), "lse")
+        if workspace is None:
+            workspace = new_cross_attn_workspace(q, k)
+        _need(workspace, torch.uint8, None, "workspace")
+        for n, t in (("k", k), ("v", v), ("k_len", k_len), ("out", out), ("lse", lse), ("workspace", workspace)):
+            _on(q.device, n, t)
+        _check(load().cross_attn_fwd(s, Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(k_len), ctypes.c_float(softmax_scale),
+                                     _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return (out, lse) if with_lse else out

@@ -11,18 +11,14 @@
 #include <string>
 
 #include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
 
-#include "common.cuh"
-
-namespace bsva {
-}
+#include "api.cuh"
 
 using namespace bsva;
 
-namespace {
+namespace bsva {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -43,18 +39,6 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(BSVA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-// An NVTX range over one entry point (its validation, descriptor encoding and
-// launches), named after the entry, so that a profiler timeline shows which
-// call issued which kernels. NVTX costs nothing measurable when no tool is attached.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-#define BSVA_RANGE(name) NvtxRange bsva_nvtx_range_(name)
-
-
 // ------------------------------------------------------------- device check
 int check_device() {
   int dev = -1;
@@ -71,8 +55,6 @@ int check_device() {
 }
 
 // ------------------------------------------------------------ validation
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int check_shape(const bsva_shape& s) {
   if (s.B < 1 || s.H < 1 || s.Lq < 1 || s.Lk < 1)
     return fail(BSVA_ERR_INVALID_ARG, "shape: B, H, Lq, Lk must be >= 1 (got %d, %d, %d, %d)", s.B, s.H, s.Lq, s.Lk);
@@ -86,11 +68,16 @@ int check_shape(const bsva_shape& s) {
   return BSVA_OK;
 }
 
-#define REQUIRE_PTR(p, align)                                                                          \
-  do {                                                                                                 \
-    if ((p) == nullptr) return fail(BSVA_ERR_INVALID_ARG, "%s is NULL", #p);                           \
-    if (!aligned((p), (align))) return fail(BSVA_ERR_INVALID_ARG, "%s is not %d-byte aligned", #p, (align)); \
-  } while (0)
+int check_workspace(void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr) return fail(BSVA_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+  if (!aligned(ws, 256)) return fail(BSVA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (bytes < need) return fail(BSVA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+  return BSVA_OK;
+}
+
+}  // namespace bsva
+
+namespace {
 
 // ----------------------------------------------------------- tensor maps
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -119,13 +106,6 @@ int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int ele
   CUresult r = g_encode(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BSVA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, int(r));
-  return BSVA_OK;
-}
-
-int check_workspace(void* ws, size_t bytes, size_t need) {
-  if (ws == nullptr) return fail(BSVA_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
-  if (!aligned(ws, 256)) return fail(BSVA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (bytes < need) return fail(BSVA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
   return BSVA_OK;
 }
 
@@ -659,8 +639,8 @@ int bsva_check_status(void* workspace, bsva_stream_t stream) {
   if (word & kStatusTimeout)
     return fail(BSVA_ERR_DEVICE_TIMEOUT, "a device-side wait ran out of time; outputs of that call are invalid");
   if (word & kStatusBounds)
-    return fail(BSVA_ERR_DEVICE_BOUNDS, "a device-side index check failed (kept count, kept list or table row out "
-                                        "of range); outputs of that call are invalid");
+    return fail(BSVA_ERR_DEVICE_BOUNDS, "a device-side index check failed (kept count, kept list, table row, page or "
+                                        "sequence length out of range); outputs of that call are invalid");
   return ok();
 }
 

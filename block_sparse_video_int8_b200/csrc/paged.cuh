@@ -1,0 +1,147 @@
+// paged.cuh -- what the paged-cache kernels share: the description of a call (pages, sequences, query
+// rows), the checked view of one sequence, the address of a cached key, and the exact widening of
+// INT8 codes to 16-bit floats.
+#pragma once
+
+#include "common.cuh"
+
+namespace bsva {
+
+// One call. Two sources of keys go through the same kernels:
+//  - pages: row (page, head, offset) of k and v, found through page_table (page_shift = log2(page_size));
+//  - contiguous [S, Hkv, max_kv, d] tensors (cross attention): page_table null, sequence s is "page" s.
+// q_start null: every sequence has max_q query rows; kv_len null: max_kv keys.
+struct PagedArgs {
+  const void* k;
+  const void* v;                // int8 codes or bf16
+  const float* k_scale;         // [n_pages, Hkv, page_size], INT8 only
+  const float* v_scale;
+  const int32_t* q_start;       // [S + 1]
+  const int32_t* kv_len;        // [S]
+  const int32_t* page_table;    // [S, max_pages]
+  const __nv_bfloat16* q;       // element strides below
+  __nv_bfloat16* out;
+  float* lse;                   // [out rows], nullable
+  float* part_o;                // [nsplit, out rows, d] unnormalised partial outputs
+  float2* part_ml;              // [nsplit, out rows] (running max in log2 units, sum)
+  uint32_t* status;
+  long long q_seq, q_tok, q_head;   // q strides (q_seq: contiguous source only)
+  long long o_seq, o_tok, o_head;   // out strides; out row index = offset / d
+  long long out_rows;
+  float scale_log2;             // softmax scale * log2(e)
+  int n_pages, page_shift, max_pages, page_rows;   // page_rows: rows a page holds
+  int S, T, Hkv, G, d;
+  int max_q, max_kv;
+  int causal, window;
+  int nsplit, split_keys;       // rows kernel: keys of a split; tile kernel: splits share a row tile's key tiles
+  uint64_t wait_limit_ns;
+};
+
+// A sequence as the kernels use it. Values that the caller's device arrays hold are clamped into the
+// ranges that the host checked the buffers for, and a value outside records kStatusBounds: no access
+// leaves its buffer whatever the arrays say.
+struct SeqView {
+  int n;     // new tokens (query rows a head)
+  int kv;    // keys
+  int q0;    // first row of the sequence in the packed tensors
+};
+
+__device__ __forceinline__ SeqView seq_view(const PagedArgs& a, int s) {
+  SeqView r;
+  bool bad = false;
+  if (a.q_start) {
+    const int lo = a.q_start[s], hi = a.q_start[s + 1];
+    r.q0 = min(max(lo, 0), a.T);
+    r.n = min(min(max(hi, r.q0), a.T) - r.q0, a.max_q);
+    bad = r.q0 != lo || r.n != hi - lo;
+  } else {
+    r.q0 = 0;
+    r.n = a.max_q;
+  }
+  if (a.kv_len) {
+    const int kv = a.kv_len[s];
+    r.kv = min(max(kv, 0), a.max_kv);
+    bad = bad || kv != r.kv;
+  } else {
+    r.kv = a.max_kv;
+  }
+  if (bad) atomicOr(a.status, kStatusBounds);
+  return r;
+}
+
+// The page that holds token t of sequence s; an entry outside [0, n_pages) is recorded and read as page 0.
+__device__ __forceinline__ int page_of(const PagedArgs& a, int s, int t) {
+  if (!a.page_table) return s;
+  int p = __ldg(a.page_table + size_t(s) * a.max_pages + (t >> a.page_shift));
+  if (unsigned(p) >= unsigned(a.n_pages)) {
+    atomicOr(a.status, kStatusBounds);
+    p = 0;
+  }
+  return p;
+}
+
+// Row index (of d elements, or of one scale) of token t of a head, in the page that page_of gave.
+__device__ __forceinline__ size_t kv_row(const PagedArgs& a, int page, int head, int t) {
+  const int off = a.page_table ? t & ((1 << a.page_shift) - 1) : t;
+  return (size_t(page) * a.Hkv + head) * a.page_rows + off;
+}
+
+// ---- widening: each 32-bit word holds four INT8 codes b0..b3; the two results hold the pairs (b0, b2)
+// and (b1, b3). Callers choose which element sits in which byte, or which order the pairs stand for.
+// bf16: 0x4300 | (b & 0x7f) = 128 + (b & 0x7f) and 0x4300 | (b & 0x80) = 128 or 256; the difference is
+// the signed code, exactly (all terms are integers of at most 8 bits).
+__device__ __forceinline__ uint32_t lop_and_or(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(o));   // (x & m) | o
+  return r;
+}
+__device__ __forceinline__ uint32_t lop_and_xor(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(m), "r"(o));   // (x & m) ^ o
+  return r;
+}
+__device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  auto half = [](uint32_t x) {
+    uint32_t lo = lop_and_or(x, 0x007f007fu, 0x43004300u), hi = lop_and_or(x, 0x00800080u, 0x43004300u);
+    __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&lo), *reinterpret_cast<__nv_bfloat162*>(&hi));
+    return *reinterpret_cast<uint32_t*>(&d);
+  };
+  even = half(w);
+  odd = half(w >> 8);
+}
+// f16: 0x6400 | (b + 128) = 1024 + 128 + b, minus 1152.
+__device__ __forceinline__ void widen_f16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  auto half = [](uint32_t x) {
+    uint32_t v = lop_and_xor(x, 0x00ff00ffu, 0x64806480u);
+    __half2 d = __hsub2(*reinterpret_cast<__half2*>(&v), __floats2half2_rn(1152.f, 1152.f));
+    return *reinterpret_cast<uint32_t*>(&d);
+  };
+  even = half(w);
+  odd = half(w >> 8);
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---- INT8 values in an f16 product: a weight enters as w = p * s_v * c with c a power of two, so that w
+// fits f16 whatever the scales' range (c = 1 / 2^floor(log2 s), s the largest scale seen when c was set:
+// p <= 2^8 by the lazy running max, s_v * c < 2^7 by kScaleGrow, so w < 2^15). f16 keeps 11 bits of a
+// weight where bf16 would keep 8; the sum of the weights takes p itself, in fp32.
+constexpr float kScaleGrow = 128.f;   // s_v * c reaches this: c is set anew and the output so far rescaled
+__device__ __forceinline__ float scale_norm(float s) {   // 2^-floor(log2 s), both in the normal range
+  const int e = min(max(int(__float_as_uint(s) >> 23), 1), 253);
+  return __uint_as_float(uint32_t(254 - e) << 23);
+}
+
+cudaError_t launch_paged_write(const PagedArgs& a, bool int8, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                               long long k_stride, long long v_stride, cudaStream_t st);
+cudaError_t launch_paged_read(const PagedArgs& a, bool int8, const int32_t* first, int L, __nv_bfloat16* k_out,
+                              __nv_bfloat16* v_out, cudaStream_t st);
+cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st);
+cudaError_t launch_paged_tiles(const PagedArgs& a, bool int8, cudaStream_t st);
+cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st);
+
+}  // namespace bsva

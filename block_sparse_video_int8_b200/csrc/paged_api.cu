@@ -1,0 +1,260 @@
+// paged_api.cu -- the C entries of the paged K/V cache and of cross attention (include/bsva.h): argument
+// checks, the split of a call over the GPU, workspace carving and launches.
+#include <cmath>
+
+#include "api.cuh"
+#include "paged.cuh"
+
+using namespace bsva;
+
+namespace {
+
+constexpr int kMaxSplits = 64;
+
+int ilog2(int x) {
+  int r = 0;
+  while ((1 << r) < x) ++r;
+  return r;
+}
+
+int check_cache(const bsva_paged_kv* c) {
+  if (c == nullptr) return fail(BSVA_ERR_INVALID_ARG, "cache is NULL");
+  if (c->d != 64 && c->d != 128) return fail(BSVA_ERR_UNSUPPORTED, "head dim d = %d; supported: 64, 128", c->d);
+  if (c->H < 1 || c->H > 65535) return fail(BSVA_ERR_INVALID_ARG, "cache: H = %d", c->H);
+  if (c->n_pages < 1) return fail(BSVA_ERR_INVALID_ARG, "cache: n_pages = %d", c->n_pages);
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return fail(BSVA_ERR_INVALID_ARG, "page_size = %d; supported: 16, 32, 64, 128, 256", c->page_size);
+  if (c->dtype != BSVA_KV_INT8 && c->dtype != BSVA_KV_BF16)
+    return fail(BSVA_ERR_INVALID_ARG, "cache dtype = %d; use BSVA_KV_INT8 (0) or BSVA_KV_BF16 (1)", c->dtype);
+  return BSVA_OK;
+}
+
+int check_cache_ptrs(const bsva_paged_kv* c) {
+  REQUIRE_PTR(c->k, 16); REQUIRE_PTR(c->v, 16);
+  if (c->dtype == BSVA_KV_INT8) { REQUIRE_PTR(c->k_scale, 4); REQUIRE_PTR(c->v_scale, 4); }
+  return BSVA_OK;
+}
+
+int check_batch(const bsva_paged_kv* c, const bsva_paged_batch* b) {
+  if (b == nullptr) return fail(BSVA_ERR_INVALID_ARG, "batch is NULL");
+  if (b->S < 1 || b->S > 65535) return fail(BSVA_ERR_INVALID_ARG, "batch: S = %d outside [1, 65535]", b->S);
+  if (b->T < 0 || b->max_q < 1 || b->max_q > (1 << 24))
+    return fail(BSVA_ERR_INVALID_ARG, "batch: T = %d, max_q = %d (T >= 0, 1 <= max_q <= 2^24)", b->T, b->max_q);
+  if (b->max_kv < 1 || b->max_kv > (1 << 30)) return fail(BSVA_ERR_INVALID_ARG, "batch: max_kv = %d", b->max_kv);
+  if (b->max_pages < 1 || (long long)b->max_pages * c->page_size < b->max_kv)
+    return fail(BSVA_ERR_INVALID_ARG, "batch: max_pages = %d pages of %d tokens hold less than max_kv = %d", b->max_pages,
+                c->page_size, b->max_kv);
+  return BSVA_OK;
+}
+
+int check_heads(int Hq, int Hkv, long long max_q) {
+  if (Hkv < 1 || Hq < 1 || Hq > 65535 || Hq % Hkv)
+    return fail(BSVA_ERR_INVALID_ARG, "Hq = %d is not a positive multiple of %d key heads", Hq, Hkv);
+  if (max_q * (Hq / Hkv) > (1ll << 30))
+    return fail(BSVA_ERR_INVALID_ARG, "%lld query rows of %d heads a key head are too many for one call", max_q, Hq / Hkv);
+  return BSVA_OK;
+}
+
+// How a call is laid over the GPU. Few rows leave few CTAs, so their keys are split and joined by a second
+// kernel; the number of splits follows from the host bounds alone.
+struct Plan {
+  int nsplit = 1, split_keys = 0;
+  int cap = 1;   // >= nsplit, and no smaller for more keys: workspaces are sized by it
+};
+
+Plan make_plan(int S, int Hkv, int G, int max_q, int keys) {
+  Plan p;
+  const long long rows = (long long)max_q * G, nr = rows <= 8 ? 8 : 16;
+  const long long items = (rows + nr - 1) / nr * Hkv * S;
+  const long long want = 148 * 8;
+  long long n = (want + items - 1) / items;
+  const long long most = (keys + 127) / 128;      // a split has 128 keys at least: two blocks a warp
+  n = n < most ? n : most;
+  n = n < kMaxSplits ? n : kMaxSplits;
+  n = n < 1 ? 1 : n;
+  p.cap = int(n);
+  const long long per = ((keys + n - 1) / n + 63) / 64 * 64;
+  p.split_keys = int(per);
+  p.nsplit = int((keys + per - 1) / per);
+  return p;
+}
+
+size_t align256z(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Status word, then the partial outputs and their (max, sum) pairs.
+struct PagedWs {
+  size_t part_o = 256, part_ml = 0, total = 256;
+  PagedWs(int cap, size_t out_rows, int d) {
+    if (cap < 2) return;
+    part_ml = align256z(part_o + size_t(cap) * out_rows * d * 4);
+    total = align256z(part_ml + size_t(cap) * out_rows * 8);
+  }
+};
+
+void fill_cache(PagedArgs& a, const bsva_paged_kv* c, const bsva_paged_batch* b) {
+  a.k = c->k; a.v = c->v; a.k_scale = c->k_scale; a.v_scale = c->v_scale;
+  a.q_start = b->q_start; a.kv_len = b->kv_len; a.page_table = b->page_table;
+  a.n_pages = c->n_pages; a.page_shift = ilog2(c->page_size); a.page_rows = c->page_size; a.max_pages = b->max_pages;
+  a.S = b->S; a.T = b->T; a.Hkv = c->H; a.G = 1; a.d = c->d; a.max_q = b->max_q; a.max_kv = b->max_kv;
+  a.wait_limit_ns = kWaitLimitNs;
+}
+
+int run_paged(PagedArgs& a, bool int8, const Plan& p, const PagedWs& w, void* workspace, cudaStream_t st) {
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.nsplit = p.nsplit;
+  a.split_keys = p.split_keys;
+  a.part_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
+  a.part_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + w.part_ml) : nullptr;
+  cudaError_t e = launch_paged_rows(a, int8, st);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  if (p.nsplit > 1) {
+    e = launch_paged_combine(a, st);
+    if (e != cudaSuccess) return cuda_fail(e, "split combination launch");
+  }
+  return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bsva_paged_workspace_bytes(const bsva_paged_kv* c, const bsva_paged_batch* b, int Hq) {
+  if (check_cache(c) || check_batch(c, b) || check_heads(Hq, c->H, b->max_q)) return 0;
+  return PagedWs(make_plan(b->S, c->H, Hq / c->H, b->max_q, b->max_kv).cap, size_t(b->T) * Hq, c->d).total;
+}
+
+int bsva_paged_kv_write(const bsva_paged_kv* c, const bsva_paged_batch* b, const void* k, const void* v,
+                        long long k_stride, long long v_stride, void* workspace, size_t workspace_bytes,
+                        bsva_stream_t stream) {
+  BSVA_RANGE("bsva_paged_kv_write");
+  int rc;
+  if ((rc = check_cache(c)) || (rc = check_cache_ptrs(c)) || (rc = check_batch(c, b))) return rc;
+  REQUIRE_PTR(b->q_start, 4); REQUIRE_PTR(b->kv_len, 4); REQUIRE_PTR(b->page_table, 4);
+  if ((rc = check_heads(c->H, c->H, (long long)b->max_q * c->H))) return rc;
+  if (k_stride < (long long)c->H * c->d || v_stride < (long long)c->H * c->d || k_stride % 8 || v_stride % 8)
+    return fail(BSVA_ERR_INVALID_ARG, "token strides %lld, %lld must be multiples of 8 and at least H*d = %d", k_stride,
+                v_stride, c->H * c->d);
+  if (b->T > 0) { REQUIRE_PTR(k, 16); REQUIRE_PTR(v, 16); }
+  if ((rc = check_workspace(workspace, workspace_bytes, 256))) return rc;
+  if ((rc = check_device())) return rc;
+  if (b->T == 0) return ok();
+  PagedArgs a{};
+  fill_cache(a, c, b);
+  a.status = static_cast<uint32_t*>(workspace);
+  cudaError_t e = launch_paged_write(a, c->dtype == BSVA_KV_INT8, static_cast<const __nv_bfloat16*>(k),
+                                     static_cast<const __nv_bfloat16*>(v), k_stride, v_stride,
+                                     reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged write launch");
+  return ok();
+}
+
+int bsva_paged_kv_read(const bsva_paged_kv* c, const bsva_paged_batch* b, const int32_t* first, int L, void* k_out,
+                       void* v_out, void* workspace, size_t workspace_bytes, bsva_stream_t stream) {
+  BSVA_RANGE("bsva_paged_kv_read");
+  int rc;
+  if ((rc = check_cache(c)) || (rc = check_cache_ptrs(c)) || (rc = check_batch(c, b))) return rc;
+  REQUIRE_PTR(b->kv_len, 4); REQUIRE_PTR(b->page_table, 4);
+  if (first && !aligned(first, 4)) return fail(BSVA_ERR_INVALID_ARG, "first is not 4-byte aligned");
+  if (L < 1 || L > (1 << 30)) return fail(BSVA_ERR_INVALID_ARG, "L = %d", L);
+  REQUIRE_PTR(k_out, 16); REQUIRE_PTR(v_out, 16);
+  if ((rc = check_workspace(workspace, workspace_bytes, 256))) return rc;
+  if ((rc = check_device())) return rc;
+  PagedArgs a{};
+  fill_cache(a, c, b);
+  a.q_start = nullptr;
+  a.status = static_cast<uint32_t*>(workspace);
+  cudaError_t e = launch_paged_read(a, c->dtype == BSVA_KV_INT8, first, L, static_cast<__nv_bfloat16*>(k_out),
+                                    static_cast<__nv_bfloat16*>(v_out), reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged read launch");
+  return ok();
+}
+
+int paged_attn_fwd(const bsva_paged_kv* c, const bsva_paged_batch* b, const void* q, long long q_stride, int Hq,
+                   int causal, int window, float softmax_scale, void* out, float* lse, void* workspace,
+                   size_t workspace_bytes, bsva_stream_t stream) {
+  BSVA_RANGE("paged_attn_fwd");
+  int rc;
+  if ((rc = check_cache(c)) || (rc = check_cache_ptrs(c)) || (rc = check_batch(c, b))) return rc;
+  REQUIRE_PTR(b->q_start, 4); REQUIRE_PTR(b->kv_len, 4); REQUIRE_PTR(b->page_table, 4);
+  if ((rc = check_heads(Hq, c->H, b->max_q))) return rc;
+  if (q_stride < (long long)Hq * c->d || q_stride % 8)
+    return fail(BSVA_ERR_INVALID_ARG, "token stride %lld must be a multiple of 8 and at least Hq*d = %d", q_stride,
+                Hq * c->d);
+  if (causal != 0 && causal != 1) return fail(BSVA_ERR_INVALID_ARG, "causal = %d; use 0 or 1", causal);
+  if (window < 0 || (window > 0 && !causal))
+    return fail(BSVA_ERR_INVALID_ARG, "window = %d must be >= 0, and 0 without causal", window);
+  if (std::isnan(softmax_scale) || std::isinf(softmax_scale))
+    return fail(BSVA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (lse && !aligned(lse, 4)) return fail(BSVA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  if (b->T > 0) { REQUIRE_PTR(q, 16); REQUIRE_PTR(out, 16); }
+  const size_t rows = size_t(b->T) * Hq;
+  const PagedWs w(make_plan(b->S, c->H, Hq / c->H, b->max_q, b->max_kv).cap, rows, c->d);
+  if ((rc = check_workspace(workspace, workspace_bytes, w.total))) return rc;
+  if ((rc = check_device())) return rc;
+  if (b->T == 0) return ok();
+  PagedArgs a{};
+  fill_cache(a, c, b);
+  a.G = Hq / c->H;
+  a.q = static_cast<const __nv_bfloat16*>(q); a.q_tok = q_stride; a.q_head = c->d;
+  a.out = static_cast<__nv_bfloat16*>(out); a.o_tok = (long long)Hq * c->d; a.o_head = c->d;
+  a.lse = lse;
+  a.out_rows = (long long)rows;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(float(c->d));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.causal = causal;
+  a.window = window;
+  // keys a sequence's rows can see: with a window, its width and the chunk's length (from a multiple of 16)
+  const long long reach = window ? (long long)window + b->max_q + 15 : b->max_kv;
+  const Plan p = make_plan(b->S, c->H, a.G, b->max_q, reach < b->max_kv ? int(reach) : b->max_kv);
+  return run_paged(a, c->dtype == BSVA_KV_INT8, p, w, workspace,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+static int check_cross(const bsva_shape& s, int Hkv) {
+  int rc;
+  if ((rc = check_shape(s))) return rc;
+  return check_heads(s.H, Hkv, s.Lq);
+}
+
+size_t bsva_cross_attn_workspace_bytes(bsva_shape s, int Hkv) {
+  s.n_prefix = 0;
+  if (check_cross(s, Hkv)) return 0;
+  return PagedWs(make_plan(s.B, Hkv, s.H / Hkv, s.Lq, s.Lk).cap, size_t(s.B) * s.H * s.Lq, s.d).total;
+}
+
+int cross_attn_fwd(bsva_shape s, int Hkv, const void* q, const void* k, const void* v, const int32_t* k_len,
+                   float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                   bsva_stream_t stream) {
+  BSVA_RANGE("cross_attn_fwd");
+  int rc;
+  s.n_prefix = 0;
+  if ((rc = check_cross(s, Hkv))) return rc;
+  if (std::isnan(softmax_scale) || std::isinf(softmax_scale))
+    return fail(BSVA_ERR_INVALID_ARG, "softmax_scale must be finite");
+  REQUIRE_PTR(q, 16); REQUIRE_PTR(k, 16); REQUIRE_PTR(v, 16); REQUIRE_PTR(out, 16);
+  if (k_len && !aligned(k_len, 4)) return fail(BSVA_ERR_INVALID_ARG, "k_len is not 4-byte aligned");
+  if (lse && !aligned(lse, 4)) return fail(BSVA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  const Plan p = make_plan(s.B, Hkv, s.H / Hkv, s.Lq, s.Lk);
+  const size_t rows = size_t(s.B) * s.H * s.Lq;
+  const PagedWs w(p.cap, rows, s.d);
+  if ((rc = check_workspace(workspace, workspace_bytes, w.total))) return rc;
+  if ((rc = check_device())) return rc;
+  PagedArgs a{};
+  a.k = k; a.v = v; a.kv_len = k_len;
+  a.n_pages = s.B; a.page_rows = s.Lk;
+  a.S = s.B; a.Hkv = Hkv; a.G = s.H / Hkv; a.d = s.d; a.max_q = s.Lq; a.max_kv = s.Lk;
+  a.wait_limit_ns = kWaitLimitNs;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.q_seq = a.o_seq = (long long)s.H * s.Lq * s.d;
+  a.q_tok = a.o_tok = s.d;
+  a.q_head = a.o_head = (long long)s.Lq * s.d;
+  a.lse = lse;
+  a.out_rows = (long long)rows;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(float(s.d));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return run_paged(a, false, p, w, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,396 @@
+// paged_rows.cu -- attention of few query rows (single tokens, short chunks) over cached keys, split over
+// the keys, and the kernel that joins the splits.
+//
+// o_i = sum_t p_it v_t / sum_t p_it, p_it = 2^(x_it - m_i), x_it = scale * log2(e) * (q_i . k_t), over the
+// keys t that row i may see (t <= pos_i when causal, t > pos_i - window); m_i the running maximum.
+//
+// The query heads of one key head share its keys: row r of (sequence, key head) is token r / G, head
+// r % G. One CTA = (row tile of 8 * NT rows, split of the keys, key head, sequence); its four warps take
+// 16-key blocks in turn, each with its own running maximum, sum and output, and join at the end.
+// Such calls are bound by reading the codes (an INT8 key head's token is 2 d + 8 bytes for 4 d flops a
+// row), so codes go from global memory straight into registers, in an order that is already that of the
+// tensor-core fragments, and both products have the keys' data on the 16-row side, so that 8 rows waste
+// nothing:
+//   S^T [16 keys x 8 rows] += K [16 x 16] . Q^T [16 x 8]        (bf16; INT8 codes widened, exact)
+//   O^T [16 d   x 8 rows] += V^T [16 x 16 keys] . P^T [16 x 8]  (f16 for INT8 codes, bf16 for bf16 values)
+// A product's inner index may run in any order that both operands share, and so may the d index of O:
+//   lane (g = lane / 4, t = lane % 4) reads 16-byte pieces of key rows g and g + 8 and takes four
+//   consecutive d values a step; of V it reads d values [g d/8, (g + 1) d/8) of keys 2t, 2t+1, 2t+8, 2t+9.
+// The loads of the next block's K are issued as soon as this block's codes are consumed, then V's.
+#include <climits>
+
+#include "paged.cuh"
+
+namespace bsva {
+namespace {
+
+constexpr int kRowThreads = 128;
+constexpr float kLazy = 8.f;   // the running maximum is raised when some logit passes it by 2^8
+
+template <bool F16>
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit values across the warp: lane (g, t) gives row g, columns 2t, 2t+1.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <int D, bool I8, int NT>
+__global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs a) {
+  constexpr int KS = D / 16;              // steps of 16 d values in q . k
+  constexpr int EB = I8 ? 1 : 2;          // bytes of a cached value
+  constexpr int KL = D * EB / 64;         // 16-byte loads of a lane from one key row
+  constexpr int VB = D / 8 * EB;          // bytes of a lane's d values of one V row (8, 16 or 32)
+  constexpr int VW = VB / 4;              // ... in words
+  constexpr int MT = D / 16;              // 16-row tiles of O^T
+  const int s = blockIdx.z, h = blockIdx.y;
+  const int rt = blockIdx.x / a.nsplit, sp = blockIdx.x % a.nsplit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  const SeqView sv = seq_view(a, s);
+  const int R = sv.n * a.G;               // rows of this (sequence, key head)
+  const int rb = rt * 8 * NT;             // first row of the tile
+  if (rb >= R) return;
+  const int i0 = rb / a.G, i1 = (min(rb + 8 * NT, R) - 1) / a.G;   // tokens of the tile's rows
+  // keys that some row of the tile sees, and this split's part of them (from a multiple of 16)
+  const int past = sv.kv - sv.n;
+  const int hi_all = a.causal ? min(sv.kv, past + i1 + 1) : sv.kv;
+  const int lo_all = a.window ? max(0, past + i0 - a.window + 1) & ~15 : 0;
+  const int lo = min((long long)lo_all + (long long)sp * a.split_keys, (long long)INT_MAX - 64);
+  const int hi = min((long long)hi_all, (long long)lo + a.split_keys);
+
+  // this lane's rows as columns of the products: 8 nt + 2t and + 1; what each sees
+  int see_lo[NT][2], see_hi[NT][2];       // first and last key
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = min(rb + 8 * nt + 2 * t + e, R - 1);
+      const int pos = past + r / a.G;
+      see_hi[nt][e] = a.causal ? min(pos, sv.kv - 1) : sv.kv - 1;
+      see_lo[nt][e] = a.window ? max(0, pos - a.window + 1) : 0;
+    }
+  // blocks in [full_lo, full_hi) need no mask: every row of the tile sees all of them
+  const int full_lo = a.window ? max(0, past + i1 - a.window + 1) : 0;
+  const int full_hi = a.causal ? min(sv.kv, past + i0 + 1) : sv.kv;
+
+  // q as the B operand: lane (g, t) holds row 8 nt + g, the d values its key pieces have
+  uint32_t bq[NT][KS][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = rb + 8 * nt + g;
+    const bool have = r < R;
+    const __nv_bfloat16* qp = a.q + (long long)s * a.q_seq + (long long)(sv.q0 + (have ? r / a.G : 0)) * a.q_tok +
+                              (long long)(h * a.G + (have ? r % a.G : 0)) * a.q_head;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      // four consecutive d values: INT8 pieces hold 16 of them, bf16 pieces 8
+      const int d0 = I8 ? (kk / 4) * 64 + 16 * t + 4 * (kk % 4) : (kk / 2) * 32 + 8 * t + 4 * (kk % 2);
+      const uint2 w = have ? __ldg(reinterpret_cast<const uint2*>(qp + d0)) : make_uint2(0, 0);
+      bq[nt][kk][0] = I8 ? __byte_perm(w.x, w.y, 0x5410) : w.x;   // INT8: (d0, d0+2), (d0+1, d0+3)
+      bq[nt][kk][1] = I8 ? __byte_perm(w.x, w.y, 0x7632) : w.y;
+    }
+  }
+
+  float m[NT][2], l[NT][2], o[NT][MT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.f;
+  }
+  float cn = 0.f;                         // INT8: the scales' power of two (0: not set yet)
+
+  uint4 kr[2][KL];
+  uint32_t vr[4][VW];
+  float ks[2], vs[2];
+  const char* kbase = static_cast<const char*>(a.k);
+  const char* vbase = static_cast<const char*>(a.v);
+  size_t row = 0;                         // first row of the block whose loads come next
+  auto locate = [&](int key) { row = key < hi ? kv_row(a, page_of(a, s, key), h, key) : 0; };
+  auto load_k = [&](int key) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool in = key + g + 8 * e < hi;
+      const uint4* p = reinterpret_cast<const uint4*>(kbase + (row + g + 8 * e) * (D * EB)) + t;
+#pragma unroll
+      for (int c = 0; c < KL; ++c) kr[e][c] = in ? __ldg(p + 4 * c) : make_uint4(0, 0, 0, 0);
+      if constexpr (I8) ks[e] = in ? __ldg(a.k_scale + row + g + 8 * e) * a.scale_log2 : 0.f;
+    }
+  };
+  auto load_v = [&](int key) {            // zeros behind the last key: what stale rows hold must not reach O
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kk = 2 * t + (e & 1) + 8 * (e >> 1);
+      const bool in = key + kk < hi;
+      const char* p = vbase + (row + kk) * (D * EB) + g * VB;
+      if constexpr (VB == 8) {
+        const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+        vr[e][0] = x.x; vr[e][1] = x.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < VB / 16; ++c) {
+          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(p) + c) : make_uint4(0, 0, 0, 0);
+          vr[e][4 * c] = x.x; vr[e][4 * c + 1] = x.y; vr[e][4 * c + 2] = x.z; vr[e][4 * c + 3] = x.w;
+        }
+      }
+    }
+    if constexpr (I8) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) vs[e] = key + g + 8 * e < hi ? __ldg(a.v_scale + row + g + 8 * e) : 0.f;
+    }
+  };
+
+  constexpr int STEP = 16 * (kRowThreads / 32);
+  int key = lo + 16 * warp;
+  if (key < hi) {
+    locate(key);
+    load_k(key);
+    load_v(key);
+  }
+  for (; key < hi; key += STEP) {
+    // ---- logits of 16 keys, in log2 units: lane holds keys g (e = 0, 1) and g + 8 (e = 2, 3)
+    float x[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      uint32_t a0, a1, a2, a3;
+      if constexpr (I8) {
+        const uint32_t* w0 = &kr[0][kk / 4].x + kk % 4;
+        const uint32_t* w1 = &kr[1][kk / 4].x + kk % 4;
+        widen_bf16(*w0, a0, a2);
+        widen_bf16(*w1, a1, a3);
+      } else {
+        const uint32_t* w0 = &kr[0][kk / 2].x + 2 * (kk % 2);
+        const uint32_t* w1 = &kr[1][kk / 2].x + 2 * (kk % 2);
+        a0 = w0[0]; a2 = w0[1];
+        a1 = w1[0]; a3 = w1[1];
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_16x8x16<false>(x[nt], a0, a1, a2, a3, bq[nt][kk][0], bq[nt][kk][1]);
+    }
+    const float f0 = I8 ? ks[0] : a.scale_log2, f1 = I8 ? ks[1] : a.scale_log2;
+    locate(key + STEP);
+    load_k(key + STEP);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      x[nt][0] *= f0; x[nt][1] *= f0;
+      x[nt][2] *= f1; x[nt][3] *= f1;
+    }
+    if (key < full_lo || key + 16 > min(full_hi, hi)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int kk = key + g + 8 * (e >> 1);
+          if (kk >= hi || kk < see_lo[nt][e & 1] || kk > see_hi[nt][e & 1]) x[nt][e] = -INFINITY;
+        }
+    }
+    // ---- raise the running maximum where a logit passes it by 2^8 (always at the first block)
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) over = over || fmaxf(x[nt][e], x[nt][e + 2]) > m[nt][e] + kLazy;
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float al[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[nt][e], x[nt][e + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+          const float mn = fmaxf(m[nt][e], mx);
+          al[e] = mn == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mn);
+          m[nt][e] = mn;
+          l[nt][e] *= al[e];
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][j][e] *= al[e & 1];
+      }
+    }
+    float c0 = 1.f, c1 = 1.f;             // INT8: weight of a key's codes, s_v * cn
+    if constexpr (I8) {
+      const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1]))));
+      if (top * cn >= kScaleGrow || (cn == 0.f && top > 0.f)) {
+        const float c = scale_norm(top), f = cn == 0.f ? 1.f : c / cn;
+        cn = c;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][j][e] *= f;
+      }
+      c0 = vs[0] * cn;
+      c1 = vs[1] * cn;
+    }
+    // ---- weights, transposed into the B operand of the second product
+    uint32_t bp[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float mu = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
+        p[e] = ex2_approx(x[nt][e] - mu);
+        l[nt][e & 1] += p[e];
+      }
+      bp[nt][0] = transpose_8x8(I8 ? pack_f16x2(p[0] * c0, p[1] * c0) : pack_bf16x2(p[0], p[1]));
+      bp[nt][1] = transpose_8x8(I8 ? pack_f16x2(p[2] * c1, p[3] * c1) : pack_bf16x2(p[2], p[3]));
+    }
+    // ---- O^T: word w of the lane's V pieces gives d values in pairs, keys (2t, 2t+1) and (2t+8, 2t+9)
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      const uint32_t a_lo = __byte_perm(vr[0][w], vr[1][w], 0x5410), a_hi = __byte_perm(vr[0][w], vr[1][w], 0x7632);
+      const uint32_t b_lo = __byte_perm(vr[2][w], vr[3][w], 0x5410), b_hi = __byte_perm(vr[2][w], vr[3][w], 0x7632);
+      if constexpr (I8) {                 // d values 4w .. 4w+3: two tiles
+        uint32_t a0, a1, a2, a3;
+        widen_f16(a_lo, a0, a1);
+        widen_f16(b_lo, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16x8x16<true>(o[nt][2 * w], a0, a1, a2, a3, bp[nt][0], bp[nt][1]);
+        widen_f16(a_hi, a0, a1);
+        widen_f16(b_hi, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16x8x16<true>(o[nt][2 * w + 1], a0, a1, a2, a3, bp[nt][0], bp[nt][1]);
+      } else {                            // d values 2w, 2w+1: one tile
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16x8x16<false>(o[nt][w], a_lo, a_hi, b_lo, b_hi, bp[nt][0], bp[nt][1]);
+      }
+    }
+    load_v(key + STEP);
+  }
+
+  // ---- join the four warps: each leaves its maximum, sum and output (over cn) in shared memory
+  constexpr int W = kRowThreads / 32, NR = 8 * NT;
+  __shared__ float s_m[W][NR], s_l[W][NR];
+  __shared__ __align__(16) float s_o[W][NR][D + 4];
+  const float inv_c = I8 && cn != 0.f ? 1.f / cn : 1.f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float ls = l[nt][e];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+      const int r = 8 * nt + 2 * t + e;
+      if (g == 0) {
+        s_m[warp][r] = m[nt][e];
+        s_l[warp][r] = ls;
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {      // lane's d values: g * D/8 + 2j, + 1
+        s_o[warp][r][g * (D / 8) + 2 * j] = o[nt][j][e] * inv_c;
+        s_o[warp][r][g * (D / 8) + 2 * j + 1] = o[nt][j][e + 2] * inv_c;
+      }
+    }
+  __syncthreads();
+  for (int x = threadIdx.x; x < NR * (D / 4); x += kRowThreads) {
+    const int r = x / (D / 4), c = x % (D / 4);
+    const int rr = rb + r;
+    if (rr >= R) continue;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[w][r]);
+    float ls = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = s_m[w][r] == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - mx);
+      const float4 z = *reinterpret_cast<const float4*>(&s_o[w][r][4 * c]);
+      ls += f * s_l[w][r];
+      y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
+    }
+    const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
+                          (long long)(h * a.G + rr % a.G) * a.o_head;
+    if (a.nsplit > 1) {
+      const size_t pr = size_t(sp) * a.out_rows + off / D;
+      *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c) = y;
+      if (c == 0) a.part_ml[pr] = make_float2(mx, ls);
+    } else {
+      const float inv = ls > 0.f ? 1.f / ls : 0.f;
+      *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
+          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+      if (c == 0 && a.lse) a.lse[off / D] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+}
+
+// Joins the splits of every output row, in their order. One group of D/4 lanes a row, 4 values a lane.
+template <int D>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
+  constexpr int LPR = D / 4;
+  const long long x = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // (token, head) of the sequence
+  const int c = threadIdx.x % LPR;
+  const int s = blockIdx.y, Hq = a.Hkv * a.G;
+  const SeqView sv = seq_view(a, s);
+  if (x >= (long long)sv.n * Hq) return;
+  const long long off = (long long)s * a.o_seq + (sv.q0 + x / Hq) * a.o_tok + (x % Hq) * a.o_head;
+  const size_t row = off / D;
+  float mx = -INFINITY;
+  for (int p = 0; p < a.nsplit; ++p) mx = fmaxf(mx, a.part_ml[size_t(p) * a.out_rows + row].x);
+  float ls = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < a.nsplit; ++p) {
+    const size_t pr = size_t(p) * a.out_rows + row;
+    const float2 ml = a.part_ml[pr];
+    if (ml.x == -INFINITY) continue;   // a split without a key of this row: its output part is not written
+    const float f = ex2_approx(ml.x - mx);
+    const float4 z = *reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c);
+    ls += f * ml.y;
+    y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
+  }
+  const float inv = ls > 0.f ? 1.f / ls : 0.f;
+  *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
+      make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  if (c == 0 && a.lse) a.lse[row] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st) {
+  const long long rows = (long long)a.max_q * a.G;
+  const int nr = rows <= 8 ? 8 : 16;
+  const dim3 grid(unsigned((rows + nr - 1) / nr * a.nsplit), a.Hkv, a.S);
+  auto go = [&](auto f) { f<<<grid, kRowThreads, 0, st>>>(a); };
+#define BSVA_ROWS(D, I8) nr == 8 ? go(paged_rows_kernel<D, I8, 1>) : go(paged_rows_kernel<D, I8, 2>)
+  if (a.d == 128) {
+    if (int8) BSVA_ROWS(128, true); else BSVA_ROWS(128, false);
+  } else {
+    if (int8) BSVA_ROWS(64, true); else BSVA_ROWS(64, false);
+  }
+#undef BSVA_ROWS
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st) {
+  const long long rows = (long long)a.max_q * a.Hkv * a.G, rpb = 256 / (a.d / 4);
+  const dim3 grid(unsigned((rows + rpb - 1) / rpb), a.S);
+  if (a.d == 128) paged_combine_kernel<128><<<grid, 256, 0, st>>>(a);
+  else paged_combine_kernel<64><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace bsva

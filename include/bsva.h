@@ -377,6 +377,108 @@ int masked_block_attn_fwd_kvcache(const bsva_kv_cache* c, int Lq, const int8_t* 
                                   void* out, float* lse, void* workspace,
                                   size_t workspace_bytes, bsva_stream_t stream);
 
+/* Paged K/V cache for causal generation: keys and values live in pages of page_size
+ * tokens, sequences own pages through a table, and one token can be appended without
+ * touching its neighbours. (The ring above moves whole slabs of one length for every
+ * batch entry; the pages have no counterpart of this one.) Query heads may share key
+ * heads: Hq is a multiple of H, query head h reads key head h / (Hq / H).
+ * BSVA_KV_INT8 holds codes with one scale per (token, head): s = fl32(amax/127) over
+ * the d values, code = rint_half_even(fl32(x/s)), 0 where s = 0; the cached value is
+ * code * s. BSVA_KV_BF16 holds the values themselves. Values must be finite.
+ * The caller allocates the buffers (not necessarily initialised: a row is read only
+ * once it has been written). */
+enum bsva_kv_dtype {
+  BSVA_KV_INT8 = 0,
+  BSVA_KV_BF16 = 1
+};
+
+typedef struct bsva_paged_kv {
+  int n_pages, page_size;   /* page_size: 16, 32, 64, 128 or 256 tokens                 */
+  int H, d;                 /* key heads; head dim 64 or 128                            */
+  int dtype;                /* bsva_kv_dtype                                            */
+  void* k;                  /* device, int8 or bf16 [n_pages, H, page_size, d]          */
+  void* v;                  /* the same                                                 */
+  float* k_scale;           /* device fp32 [n_pages, H, page_size]; NULL for bf16       */
+  float* v_scale;
+} bsva_paged_kv;
+
+/* A batch of S sequences. Sequence s has kv_len[s] tokens, new ones included; its
+ * q_start[s+1] - q_start[s] new tokens (0 allowed) are rows q_start[s] ... of the packed
+ * tensors [T, heads, d] and the last ones of the sequence. Token t lies in page
+ * page_table[s*max_pages + t/page_size], row t % page_size; entries of pages that a call
+ * does not reach (behind the last token, before the window) are not read. Pages that are
+ * read may be shared between sequences; a page that is written belongs to one.
+ * T, max_q and max_kv are host bounds on the device arrays: q_start[S] <= T, every
+ * sequence has at most max_q new tokens and max_kv tokens. They fix the launch, so a
+ * captured graph replays with other lengths below them. Device arrays that break a bound
+ * (or name a page outside the cache) leave every access inside its buffer and are
+ * reported by bsva_check_status as BSVA_ERR_DEVICE_BOUNDS; the call's outputs are then
+ * invalid. Rows of packed outputs outside [q_start[0], q_start[S]) are left as they were. */
+typedef struct bsva_paged_batch {
+  int S, T;                   /* sequences; rows of the packed tensors                  */
+  int max_q, max_kv;          /* bounds, max_q >= 1, max_kv >= 1                        */
+  int max_pages;              /* columns of page_table, max_kv <= max_pages*page_size   */
+  const int32_t* q_start;     /* device int32 [S+1], ascending                          */
+  const int32_t* kv_len;      /* device int32 [S]                                       */
+  const int32_t* page_table;  /* device int32 [S, max_pages]                            */
+} bsva_paged_batch;
+
+/* Workspace bytes of any of the paged calls for this cache and batch and up to Hq query
+ * heads; 0 on a bad geometry. Write and read need its first 256 bytes (the status word)
+ * only. Calls that may run at the same time need a workspace each. */
+size_t bsva_paged_workspace_bytes(const bsva_paged_kv* c, const bsva_paged_batch* b, int Hq);
+
+/* Writes the batch's new tokens into their pages (quantised for BSVA_KV_INT8).
+ *   k, v       bf16 [T, H, d]; k_stride, v_stride: elements between tokens, a multiple of
+ *              8 and at least H*d (a slice of a fused projection's output serves as it is)
+ * Tokens at a negative position (kv_len smaller than the chunk) are not written and
+ * reported like a broken bound. */
+int bsva_paged_kv_write(const bsva_paged_kv* c, const bsva_paged_batch* b, const void* k, const void* v,
+                        long long k_stride, long long v_stride, void* workspace,
+                        size_t workspace_bytes, bsva_stream_t stream);
+
+/* Reads tokens back as bf16 (the cached values, rounded once): row r of sequence s is
+ * token first[s] + r, zero at and after the sequence's end. The layout is that of the
+ * other entries' K and V, so that a cached context can enter them.
+ *   first      device int32 [S], NULL = 0; a start behind the end gives zeros
+ *   L          rows per sequence, >= 1; kv_len[s] - first[s] <= L
+ *   k_out, v_out  out: bf16 [S, H, L, d]
+ * q_start is not used and may be NULL; T and max_q are not used. */
+int bsva_paged_kv_read(const bsva_paged_kv* c, const bsva_paged_batch* b, const int32_t* first, int L,
+                       void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                       bsva_stream_t stream);
+
+/* Attention of the batch's new tokens over their sequences' cached keys, the new ones
+ * included (bsva_paged_kv_write first). New token i of a sequence is at position
+ * p = kv_len - n + i; it sees key t iff t < kv_len and, when causal, t <= p and
+ * (window > 0) t > p - window. A row that sees no key gets out = 0 and lse = -inf.
+ *   q          bf16 [T, Hq, d]; q_stride: elements between tokens, a multiple of 8 and at
+ *              least Hq*d
+ *   causal     0 or 1; window >= 0, 0 = none, needs causal
+ *   softmax_scale  <= 0 selects 1/sqrt(d)
+ *   out        out: bf16 [T, Hq, d];  lse out, nullable: fp32 [T, Hq] (natural log)
+ *   workspace  >= bsva_paged_workspace_bytes(c, b, Hq) bytes, 256-aligned
+ * Logits, the softmax and its sums are fp32. The result is the same on every run. */
+int paged_attn_fwd(const bsva_paged_kv* c, const bsva_paged_batch* b, const void* q, long long q_stride,
+                   int Hq, int causal, int window, float softmax_scale, void* out, float* lse,
+                   void* workspace, size_t workspace_bytes, bsva_stream_t stream);
+
+/* Workspace bytes of cross_attn_fwd for s (H query heads) with Hkv key heads; 0 on a bad
+ * geometry. */
+size_t bsva_cross_attn_workspace_bytes(bsva_shape s, int Hkv);
+
+/* Cross attention of queries to an encoder's states of another length, such as the text
+ * that conditions a video: every query sees the first k_len[b] keys of its batch entry.
+ *   s          B, H query heads, Lq, Lk, d (n_prefix is not used)
+ *   q          bf16 [B, H, Lq, d];  k, v  bf16 [B, Hkv, Lk, d], H a multiple of Hkv
+ *   k_len      device int32 [B] in [0, Lk], NULL = Lk; what padding keys and values hold
+ *              does not matter. An entry without keys gets out = 0 and lse = -inf
+ *   out        out: bf16 [B, H, Lq, d];  lse out, nullable: fp32 [B, H, Lq]
+ *   workspace  >= bsva_cross_attn_workspace_bytes(s, Hkv) bytes, 256-aligned */
+int cross_attn_fwd(bsva_shape s, int Hkv, const void* q, const void* k, const void* v, const int32_t* k_len,
+                   float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                   bsva_stream_t stream);
+
 /* masked_block_attn_fwd without a workspace. The source pages have no
  * counterpart: this entry point is for callers that cannot allocate device
  * memory, such as a plugin inside a host application whose allocator already

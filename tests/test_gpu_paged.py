@@ -1,0 +1,451 @@
+"""The paged K/V cache, chunk attention over it and cross attention on the GPU against the fp64 oracle.
+
+Tolerances (u = half a step: 2^-8 bf16, 2^-11 f16, 2^-24 fp32; A = softmax-weighted mean of |v|):
+the output's rounding 2^-8 |o|; each weight's rounding before the second product, 2^-11 A for INT8 values (f16
+weights; one below 2^-14 loses up to 2^-25 of the largest scale: n 2^-24 max|v| covers n of them) and 2^-8 A for
+bf16 values; a logit x of d products in fp32 is off by dx = (d + 4) 2^-24 scale sum|q||k|, which moves a weight by
+the factor 1 +- 2 dx and so o by 2 dx 2 A; the exponential and the fp32 sums over n keys add (n + 8) 2^-22 A.
+lse: dx + (n + 8) 2^-22 + 2^-22 |lse|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def _bf16(rng, shape, scale=1.0):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float32) * scale).to(torch.bfloat16)
+
+
+class Setup:
+    """Ragged sequences in a shuffled page pool. ``past`` tokens are placed by the test (oracle codes), the new
+    ones by ``write``. Pages and rows no token has hold poison."""
+
+    def __init__(self, bsva, lens, H, d, page, dtype, seed=0, tail=0, lead=0, poison=True, mag=1.0):
+        rng = np.random.default_rng(seed)
+        self.bsva, self.lens, self.H, self.d, self.page, self.dtype = bsva, lens, H, d, page, dtype
+        S = len(lens)
+        per = max(1, max(-(-kv // page) for _, kv in lens))
+        n_pages = sum(-(-kv // page) for _, kv in lens) + 2
+        order = np.random.default_rng(seed + 1).permutation(n_pages)   # apart from the tokens, which no page size changes
+        self.table = np.full((S, per), -7, np.int32)
+        at = 0
+        for s, (_, kv) in enumerate(lens):
+            n = -(-kv // page)
+            self.table[s, :n] = order[at:at + n]
+            at += n
+        self.kv = [[(_bf16(rng, (kv, H, d)) * torch.from_numpy(np.exp(rng.standard_normal((kv, H, 1)) * mag)
+                                                                .astype(np.float32)).to(torch.bfloat16))
+                    for _, kv in lens] for _ in range(2)]
+        starts = [lead]
+        for n, _ in lens:
+            starts.append(starts[-1] + n)
+        self.starts, self.T = starts, starts[-1] + tail
+        new = [torch.zeros((self.T, H, d), dtype=torch.bfloat16) for _ in range(2)]
+        for z in range(2):
+            for s, (n, kv) in enumerate(lens):
+                if n and kv >= n:
+                    new[z][starts[s]:starts[s + 1]] = self.kv[z][s][kv - n:]
+        self.new = [x.cuda() for x in new]
+        # the pool: poison everywhere, then the past
+        shape = (n_pages, H, page, d)
+        if dtype == torch.int8:
+            pool = [rng.integers(-127, 128, shape).astype(np.int8) for _ in range(2)]
+            scale = [np.full(shape[:3], NAN if poison else 1.0, np.float32) for _ in range(2)]
+        else:
+            pool = [np.full(shape, NAN if poison else 1.0, np.float32) for _ in range(2)]
+        self.values = [[None] * S for _ in range(2)]    # what the cache stands for, [kv, H, d] fp64
+        for z in range(2):
+            for s, (n, kv) in enumerate(lens):
+                x = self.kv[z][s].float().numpy()
+                codes, sc = paged.quantize_rows(x)
+                self.values[z][s] = paged.dequantize_rows(codes, sc) if dtype == torch.int8 else x.astype(np.float64)
+                t = np.arange(max(kv - n, 0))
+                pg = self.table[s][t // page]
+                if dtype == torch.int8:
+                    pool[z][pg, :, t % page] = codes[t]
+                    scale[z][pg, :, t % page] = sc[t]
+                else:
+                    pool[z][pg, :, t % page] = x[t]
+        if dtype == torch.int8:
+            self.cache = bsva.PagedKVCache.over(*[torch.from_numpy(x).cuda() for x in pool],
+                                                *[torch.from_numpy(x).cuda() for x in scale])
+        else:
+            self.cache = bsva.PagedKVCache.over(*[torch.from_numpy(x).to(torch.bfloat16).cuda() for x in pool])
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.batch = bsva.PagedBatch(torch.tensor(starts, **i32), torch.tensor([kv for _, kv in lens], **i32),
+                                     torch.from_numpy(self.table).cuda(), max(1, max(n for n, _ in lens)),
+                                     max(1, max(kv for _, kv in lens)))
+        self.rng = rng
+
+    def queries(self, Hq, scale=1.0):
+        return _bf16(self.rng, (self.T, Hq, self.d), scale)
+
+    def check(self, q, out, lse, causal=True, window=0, scale=None):
+        Hq = q.shape[1]
+        G = Hq // self.H
+        o_, l_ = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for s, (n, kv) in enumerate(self.lens):
+            ok = paged.visible(n, kv, causal, window)
+            rows = slice(self.starts[s], self.starts[s] + n)
+            for h in range(Hq):
+                close(q[rows, h].double().numpy(), self.values[0][s][:, h // G], self.values[1][s][:, h // G], ok,
+                      o_[rows, h], l_[rows, h], scale, self.dtype, f"sequence {s} head {h}")
+
+
+def close(q, k, v, ok, o, lse, scale, dtype, where):
+    """Compares one head's rows with the oracle within the derived bounds."""
+    n, d = q.shape
+    if n == 0:
+        return
+    sc = 1 / math.sqrt(d) if scale is None else scale
+    ro, rl, A = paged.attention_rows(q, k, v, ok, sc)
+    keys = max(1, ok.shape[1])
+    dx = ((d + 4) * 2.0 ** -24 * sc * np.where(ok, np.abs(q) @ np.abs(k).T, 0).max(1, initial=0))[:, None]
+    vmax = np.abs(np.where(ok.any(0)[:, None], v, 0)).max(initial=0)
+    u = 2.0 ** -11 if dtype == torch.int8 else 2.0 ** -8
+    tol = 2.0 ** -8 * np.abs(ro) + (u + 4 * dx + (keys + 8) * 2.0 ** -22) * A * 1.01 + 1e-38
+    if dtype == torch.int8:
+        tol += keys * 2.0 ** -24 * vmax
+    bad = ~(np.abs(o - ro) <= tol)
+    assert not bad.any(), f"{where}: {bad.sum()} of {bad.size}, worst {np.nanmax(np.abs(o - ro) / tol)} of the bound"
+    dead = ~np.isfinite(rl)
+    assert (lse[dead] == -np.inf).all() and (o[dead] == 0).all(), where
+    tl = dx[:, 0] + (keys + 8) * 2.0 ** -22 + 2.0 ** -22 * np.abs(np.where(dead, 0, rl))
+    assert (np.abs(np.where(dead, 0, lse) - np.where(dead, 0, rl)) <= np.where(dead, 1, tl)).all(), where
+
+
+def _attend(st, Hq, causal=True, window=0, scale=None, qscale=1.0, write=True):
+    if write:
+        st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(Hq, qscale)
+    ws = st.cache.new_workspace(st.batch, Hq, st.T)
+    out = torch.full((st.T, Hq, st.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((st.T, Hq), 7.0, device="cuda")
+    st.cache.attend(q.cuda(), st.batch, causal=causal, window=window, softmax_scale=scale or 0.0, with_lse=True, out=out,
+                    lse=lse, workspace=ws)
+    st.bsva.check_status(ws)
+    for x in (out, lse):       # rows before the first and behind the last sequence
+        assert (x[:st.starts[0]] == 7).all() and (x[st.starts[-1]:] == 7).all()
+    st.check(q, out, lse, causal, window, scale)
+    return q, out, lse, ws
+
+
+RAGGED = [(5, 5), (0, 17), (1, 130), (33, 100), (16, 16)]
+
+
+# ---------------------------------------------------------------------------------------- write and read
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("d,page,H", [(128, 16, 3), (64, 32, 1), (64, 256, 2), (128, 128, 5)])
+def test_write_then_read(gpu_lib, dtype, d, page, H):
+    st = Setup(gpu_lib, RAGGED, H, d, page, dtype, seed=d + page, tail=3, lead=2)
+    before = [x.clone() for x in (st.cache.k, st.cache.v)]
+    ws = st.cache.new_workspace(st.batch, H, st.T)
+    fused = torch.cat([st.new[0], st.new[1], st.new[0]], 1)      # a fused projection: k and v are slices of its rows
+    st.cache.write(fused[:, :H], fused[:, H:2 * H], st.batch, workspace=ws)
+    gpu_lib.check_status(ws)
+    for z, pool in enumerate((st.cache.k, st.cache.v)):
+        mine = torch.zeros(pool.shape[0], pool.shape[2], dtype=torch.bool)
+        for s, (n, kv) in enumerate(st.lens):
+            t = np.arange(kv)
+            pg, off = st.table[s][t // page], t % page
+            got = pool.cpu().float().numpy()[pg, :, off]
+            x = st.kv[z][s].float().numpy()
+            if dtype == torch.int8:
+                codes, sc = paged.quantize_rows(x)
+                assert np.array_equal(got, codes.astype(np.float32))
+                assert np.array_equal((st.cache.k_scale, st.cache.v_scale)[z].cpu().numpy()[pg, :, off], sc)
+            else:
+                assert np.array_equal(got, x)
+            mine[pg, off] = True
+        keep = ~mine[:, None, :, None].expand(pool.shape)
+        a, b = pool.cpu()[keep], before[z].cpu()[keep]           # rows without a token are as they were
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+    for first in (None, [0, 20, 7, 99, 3]):
+        ft = None if first is None else torch.tensor(first, dtype=torch.int32, device="cuda")
+        L = 133 if first is None else 140
+        outs = st.cache.read(st.batch, first=ft, length=L, workspace=ws)
+        gpu_lib.check_status(ws)
+        for z in range(2):
+            got = outs[z].cpu()
+            assert got.shape == (len(RAGGED), H, L, d)
+            for s, (_, kv) in enumerate(st.lens):
+                f = 0 if first is None else min(first[s], kv)
+                want = torch.from_numpy(st.values[z][s][f:].astype(np.float32)).to(torch.bfloat16).transpose(0, 1)
+                assert torch.equal(got[s, :, :kv - f], want)
+                assert (got[s, :, kv - f:] == 0).all()
+
+
+def test_write_zero_subnormal_and_tie_rows(gpu_lib):
+    st = Setup(gpu_lib, [(40, 40)], 2, 64, 16, torch.int8, seed=3)
+    x = st.new[0]
+    x[0] = 0
+    x[1] = 1e-39
+    x[2, :, ::2] = -3e-38
+    x[3] *= 2.0 ** 100
+    x[4] = (torch.arange(64, device="cuda") - 31.5).to(torch.bfloat16) * 2 + 0.0   # halves of a code against amax 127
+    x[4, :, 0] = 127
+    st.cache.write(x, x, st.batch)
+    codes, sc = paged.quantize_rows(x.float().cpu().numpy())
+    t = np.arange(40)
+    pg = st.table[0][t // 16]
+    assert np.array_equal(st.cache.k.cpu().numpy()[pg, :, t % 16], codes)
+    assert np.array_equal(st.cache.v_scale.cpu().numpy()[pg, :, t % 16], sc)
+
+
+# ---------------------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,H", [(1, 3), (5, 2), (8, 1), (3, 1)])
+def test_single_tokens(gpu_lib, dtype, d, G, H):
+    lens = [(1, 1), (1, 2), (1, 15), (1, 16), (1, 17), (1, 63), (1, 65), (1, 700), (0, 9), (1, 1003)]
+    _attend(Setup(gpu_lib, lens, H, d, 16, dtype, seed=G), G * H)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("d,page,G,H", [(64, 16, 1, 2), (128, 32, 2, 1), (128, 64, 7, 1), (64, 128, 4, 2), (128, 256, 1, 1)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 1), (True, 40), (True, 100000), (False, 0)])
+def test_chunks(gpu_lib, dtype, d, page, G, H, causal, window):
+    lens = [(5, 5), (0, 17), (1, 130), (33, 100), (16, 16), (129, 400), (2, 900), (64, 128)]
+    _attend(Setup(gpu_lib, lens, H, d, page, dtype, seed=page + G, tail=2, lead=1), G * H, causal, window)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n,kv,G,H,d,window", [(300, 2000, 1, 2, 128, 0), (257, 257, 1, 1, 64, 0), (256, 1280, 3, 1, 128, 0),
+                                               (700, 1500, 1, 1, 128, 333), (127, 5000, 2, 1, 64, 0)])
+def test_longer_chunks(gpu_lib, dtype, n, kv, G, H, d, window):
+    _attend(Setup(gpu_lib, [(n, kv)], H, d, 64, dtype, seed=n), G * H, True, window)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 200])
+def test_rows_without_keys(gpu_lib, dtype, n):
+    # sequences shorter than their chunk: the first rows see nothing; a sequence without any key
+    st = Setup(gpu_lib, [(n, n), (n, 0), (n, n // 3), (1, 0)], 2, 64, 16, dtype, seed=n)
+    st.cache.write(st.new[0], st.new[1], st.batch)      # the short ones' first tokens have no place and are reported
+    for s, (m, kv) in enumerate(st.lens):               # ... their keys are placed here
+        for z, pool in enumerate((st.cache.k, st.cache.v)):
+            for t in range(kv):
+                x = st.kv[z][s][t].float().numpy()
+                if dtype == torch.int8:
+                    c, sc = paged.quantize_rows(x)
+                    pool[st.table[s][t // 16], :, t % 16] = torch.from_numpy(c).cuda()
+                    (st.cache.k_scale, st.cache.v_scale)[z][st.table[s][t // 16], :, t % 16] = torch.from_numpy(sc).cuda()
+                else:
+                    pool[st.table[s][t // 16], :, t % 16] = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    _attend(st, 4, write=False)
+    _attend(st, 4, causal=False, write=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("qscale,mag", [(0.0, 1.0), (30.0, 1.0), (1.0, 6.0), (8.0, 3.0)])
+def test_large_logits_and_scales_of_many_sizes(gpu_lib, dtype, n, qscale, mag):
+    # equal weights; near one-hot weights; tokens whose sizes (and so scales) differ by e^12 and more
+    _attend(Setup(gpu_lib, [(n, 600), (n, 90)], 2, 128, 32, dtype, seed=n, mag=mag), 2, qscale=qscale)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_zero_rows_and_softmax_scale(gpu_lib, n):
+    st = Setup(gpu_lib, [(n, 300)], 1, 64, 16, torch.int8, seed=9)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    st.cache.v_scale.zero_()           # every value row is zero: scale 0
+    q, out, lse, _ = st.queries(2), None, None, None
+    out, lse = st.cache.attend(q.cuda(), st.batch, softmax_scale=0.3, with_lse=True)
+    assert (out == 0).all()
+    st.values[1][0][:] = 0
+    st.check(q, out, lse, scale=0.3)
+
+
+def test_page_sizes_agree_and_runs_repeat(gpu_lib):
+    # the same tokens in pages of other sizes: the keys meet in the same order, so the bits agree; and twice
+    for n in (1, 200):
+        first = None
+        for page in (16, 64, 256):
+            st = Setup(gpu_lib, [(n, 500), (min(n, 77), 77)], 2, 128, page, torch.int8, seed=4)
+            st.cache.write(st.new[0], st.new[1], st.batch)
+            q = _bf16(np.random.default_rng(1), (st.T, 4, 128)).cuda()
+            a, la = st.cache.attend(q, st.batch, with_lse=True)
+            b, lb = st.cache.attend(q, st.batch, with_lse=True)
+            assert torch.equal(a, b) and torch.equal(la, lb)
+            first = (a, la) if first is None else first
+            assert torch.equal(a, first[0]) and torch.equal(la, first[1])
+
+
+def test_generation_step_by_step(gpu_lib):
+    """Prompt, then tokens one at a time, against the whole sequence in one chunk; and the cache read back enters
+    cross attention as keys."""
+    H, G, d, page, n = 2, 3, 64, 16, 50
+    st = Setup(gpu_lib, [(n, n), (n, n)], H, d, page, torch.int8, seed=11)
+    q, out, lse, _ = _attend(st, G * H)
+    k, v = st.cache.read(st.batch)
+    one = gpu_lib.PagedKVCache(st.cache.n_pages, page, H, d)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    steps = [(0, 30)] + [(t, t + 1) for t in range(30, n)]
+    for a, b in steps:
+        m = b - a
+        batch = gpu_lib.PagedBatch(torch.tensor([0, m, 2 * m], **i32), torch.tensor([b, b], **i32), st.batch.page_table, m, b)
+        rows = torch.cat([torch.arange(a, b), torch.arange(n + a, n + b)])
+        ws = one.new_workspace(batch, G * H)
+        one.write(st.new[0][rows], st.new[1][rows], batch, workspace=ws)
+        o, ls = one.attend(q.cuda()[rows], batch, with_lse=True, workspace=ws)
+        gpu_lib.check_status(ws)
+        # two results of the same rows, each within the bounds of check(): compare both with the oracle
+        out[rows], lse[rows] = o, ls
+    st.check(q, out, lse)
+    k1, v1 = one.read(st.batch)
+    assert torch.equal(k1, k) and torch.equal(v1, v)
+    x = _bf16(np.random.default_rng(5), (2, 2, 9, d)).cuda()
+    o, ls = gpu_lib.cross_attn_fwd(x, k, v, with_lse=True)
+    for b in range(2):
+        for h in range(2):
+            close(x[b, h].double().cpu().numpy(), k[b, h].double().cpu().numpy(), v[b, h].double().cpu().numpy(),
+                  np.ones((9, n), bool), o[b, h].double().cpu().numpy(), ls[b, h].double().cpu().numpy(), None,
+                  torch.bfloat16, f"batch {b} head {h}")
+
+
+def test_prefix_pages_shared_by_sequences(gpu_lib):
+    st = Setup(gpu_lib, [(4, 100), (4, 100)], 2, 128, 32, torch.int8, seed=21)
+    table = st.table.copy()
+    table[1, :2] = table[0, :2]        # 64 tokens of prefix in common
+    st.batch.page_table.copy_(torch.from_numpy(table))
+    for z in range(2):
+        st.values[z][1][:64] = st.values[z][0][:64]
+    _attend(st, 6)
+
+
+def test_graph_replays_with_other_lengths_and_streams(gpu_lib):
+    H, G, d = 2, 4, 128
+    big = Setup(gpu_lib, [(1, 900), (1, 40), (1, 333)], H, d, 16, torch.int8, seed=31)
+    ws = big.cache.new_workspace(big.batch, G * H)
+    q = big.queries(G * H)
+    qd = q.cuda()
+    out, lse = torch.zeros_like(qd), torch.zeros((big.T, G * H), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        big.cache.write(big.new[0], big.new[1], big.batch, workspace=ws)
+        big.cache.attend(qd, big.batch, with_lse=True, out=out, lse=lse, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        big.cache.write(big.new[0], big.new[1], big.batch, workspace=ws)
+        big.cache.attend(qd, big.batch, with_lse=True, out=out, lse=lse, workspace=ws)
+    out.zero_()
+    graph.replay()
+    gpu_lib.check_status(ws)
+    big.check(q, out, lse)
+    # shorter sequences through the same graph: the tokens now cached last are attended from the new ends
+    lens = [(1, 17), (1, 40), (0, 200)]
+    big.batch.kv_len.copy_(torch.tensor([kv for _, kv in lens], dtype=torch.int32))
+    big.batch.q_start.copy_(torch.tensor([0, 1, 2, 2], dtype=torch.int32))
+    graph.replay()
+    gpu_lib.check_status(ws)
+    for z in range(2):                 # token 16 of sequence 0 was written anew
+        big.values[z][0][16] = big.values[z][0][899]
+        big.values[z][0] = big.values[z][0][:17]
+        big.values[z][2] = big.values[z][2][:200]
+    big.lens = lens
+    big.check(q, out, lse)
+
+
+# -------------------------------------------------------------------- device arrays that break their bounds
+def test_broken_bounds_are_reported_and_neighbours_are_right(gpu_lib):
+    H, d = 2, 64
+    for n in (1, 40):
+        st = Setup(gpu_lib, [(n, 120), (n, 64)], H, d, 16, torch.int8, seed=41, poison=False)
+        q, out, lse, ws = _attend(st, 4)
+        good = st.batch.page_table.clone()
+        for bad in (st.cache.n_pages, -1, 2 ** 31 - 1, -2 ** 31):
+            st.batch.page_table[0, 1] = bad
+            o, ls = st.cache.attend(q.cuda(), st.batch, with_lse=True, workspace=ws)
+            with pytest.raises(gpu_lib.BsvaError) as e:
+                gpu_lib.check_status(ws)
+            assert e.value.code == 6
+            assert torch.equal(o[n:], out[n:]) and torch.equal(ls[n:], lse[n:])
+            st.cache.read(st.batch, workspace=ws)
+            with pytest.raises(gpu_lib.BsvaError):
+                gpu_lib.check_status(ws)
+        st.batch.page_table.copy_(good)
+        st.batch.page_table[1, (64 - n) // 16] = st.cache.n_pages
+        before = st.cache.k.clone()
+        st.cache.write(st.new[0], st.new[1], st.batch, workspace=ws)
+        with pytest.raises(gpu_lib.BsvaError):
+            gpu_lib.check_status(ws)
+        assert torch.equal(before, st.cache.k)      # the others rewrote what they had, the bad one nothing
+        st.batch.page_table.copy_(good)
+        for name, bad in (("kv_len", [200, 64]), ("kv_len", [-3, 64]), ("q_start", [0, n, 2 * n + 9]),
+                          ("q_start", [5, 0, 2]), ("q_start", [-1, n, 2 * n])):
+            t = getattr(st.batch, name)
+            keep = t.clone()
+            t.copy_(torch.tensor(bad, dtype=torch.int32))
+            st.cache.attend(q.cuda(), st.batch, workspace=ws)
+            with pytest.raises(gpu_lib.BsvaError) as e:
+                gpu_lib.check_status(ws)
+            assert e.value.code == 6
+            t.copy_(keep)
+        o, ls = st.cache.attend(q.cuda(), st.batch, with_lse=True, workspace=ws)
+        gpu_lib.check_status(ws)
+        assert torch.equal(o, out)
+
+
+def test_offsets_past_32_bits(gpu_lib):
+    # a pool of more than 2^31 values, the sequence in its last pages
+    H, d, page = 8, 128, 64
+    n_pages = 2 ** 31 // (H * d * page) + 40
+    cache = gpu_lib.PagedKVCache.over(*[torch.empty((n_pages, H, page, d), dtype=torch.int8, device="cuda") for _ in range(2)],
+                                      *[torch.empty((n_pages, H, page), device="cuda") for _ in range(2)])
+    rng = np.random.default_rng(51)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for n in (1, 150):
+        k, v, q = (_bf16(rng, (200, h, d)) for h in (H, H, H))
+        table = torch.arange(n_pages - 4, n_pages, **i32)[None]
+        whole = gpu_lib.PagedBatch(torch.tensor([0, 200], **i32), torch.tensor([200], **i32), table, 200, 200)
+        cache.write(k.cuda(), v.cuda(), whole)
+        batch = gpu_lib.PagedBatch(torch.tensor([0, n], **i32), torch.tensor([200], **i32), table, n, 200)
+        out, lse = cache.attend(q[:n].cuda(), batch, with_lse=True)
+        kb, vb = cache.read(whole)
+        for h in (0, H - 1):
+            kk, vv = (paged.dequantize_rows(*paged.quantize_rows(x[:, h].float().numpy())) for x in (k, v))
+            assert torch.equal(kb[0, h].cpu(), torch.from_numpy(kk).float().to(torch.bfloat16))
+            close(q[:n, h].double().numpy(), kk, vv, paged.visible(n, 200), out[:, h].double().cpu().numpy(),
+                  lse[:, h].double().cpu().numpy(), None, torch.int8, f"n {n} head {h}")
+
+
+def test_strided_queries(gpu_lib):
+    for n in (1, 60):
+        st = Setup(gpu_lib, [(n, 200)], 2, 64, 16, torch.int8, seed=61)
+        st.cache.write(st.new[0], st.new[1], st.batch)
+        wide = _bf16(np.random.default_rng(2), (st.T, 7, 64))
+        out, lse = st.cache.attend(wide.cuda()[:, 1:5], st.batch, with_lse=True)
+        st.check(wide[:, 1:5], out, lse)
+
+
+# ------------------------------------------------------------------------------------------ cross attention
+@pytest.mark.parametrize("B,Hq,Hkv,Lq,Lk,d", [(1, 2, 2, 300, 512, 128), (3, 6, 2, 77, 33, 64), (2, 8, 1, 1, 1500, 64),
+                                              (2, 3, 3, 1, 1, 128), (1, 5, 1, 1000, 130, 128), (4, 2, 1, 9, 129, 128)])
+def test_cross_attention(gpu_lib, B, Hq, Hkv, Lq, Lk, d):
+    rng = np.random.default_rng(Lq + Lk)
+    q, k, v = _bf16(rng, (B, Hq, Lq, d)), _bf16(rng, (B, Hkv, Lk, d)), _bf16(rng, (B, Hkv, Lk, d))
+    for lens in (None, [Lk, 0, Lk // 2, 1][:B], [max(1, Lk - 1), 1, 0, Lk][:B]):
+        kd, vd = k.clone(), v.clone()
+        for b, n in enumerate(lens or []):
+            kd[b, :, n:], vd[b, :, n:] = NAN, math.inf       # what padding holds does not matter
+        kl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+        ws = gpu_lib.new_cross_attn_workspace(q.cuda(), kd.cuda())
+        o, ls = gpu_lib.cross_attn_fwd(q.cuda(), kd.cuda(), vd.cuda(), k_len=kl, with_lse=True, workspace=ws)
+        gpu_lib.check_status(ws)
+        o, ls = o.double().cpu().numpy(), ls.double().cpu().numpy()
+        for b in range(B):
+            n = Lk if lens is None else lens[b]
+            for h in range(Hq):
+                hk = h // (Hq // Hkv)
+                close(q[b, h].double().numpy(), k[b, hk, :n].double().numpy(), v[b, hk, :n].double().numpy(),
+                      np.ones((Lq, n), bool), o[b, h], ls[b, h], None, torch.bfloat16, f"batch {b} head {h}")
