@@ -75,13 +75,9 @@ int check_workspace(void* ws, size_t bytes, size_t need) {
   return BSVA_OK;
 }
 
-}  // namespace bsva
-
-namespace {
-
 // ----------------------------------------------------------- tensor maps
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
+static PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+static std::once_flag g_encode_once;
 
 int get_encoder() {
   std::call_once(g_encode_once, [] {
@@ -95,7 +91,6 @@ int get_encoder() {
   return BSVA_OK;
 }
 
-// 3-D map over [heads][rows][inner] with a box of [1][box_rows][box_inner].
 int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t inner,
                uint64_t rows, uint64_t heads, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw,
                const char* what) {
@@ -108,6 +103,10 @@ int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int ele
   if (r != CUDA_SUCCESS) return fail(BSVA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, int(r));
   return BSVA_OK;
 }
+
+}  // namespace bsva
+
+namespace {
 
 // Shared tail of both attention entry points.
 // The INT8 streaming cache as the key side of an attention launch: the K/V maps cover all

@@ -15,6 +15,10 @@ int cuda_fail(cudaError_t e, const char* what);
 int check_device();
 int check_shape(const bsva_shape& s);
 int check_workspace(void* ws, size_t bytes, size_t need);
+int get_encoder();   // the driver's tensor-map encoder, looked up once; before the first encode_map
+// 3-D map over [heads][rows][inner] with a box of [1][box_rows][box_inner].
+int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t inner, uint64_t rows,
+               uint64_t heads, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw, const char* what);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

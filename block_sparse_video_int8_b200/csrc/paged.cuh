@@ -30,11 +30,17 @@ struct PagedArgs {
   long long out_rows;
   float scale_log2;             // softmax scale * log2(e)
   int n_pages, page_shift, max_pages, page_rows;   // page_rows: rows a page holds
+  int box_rows;                 // rows of a TMA box of bf16 pages: a page's, at most a key tile's
   int S, T, Hkv, G, d;
   int max_q, max_kv;
   int causal, window;
   int nsplit, split_keys;       // rows kernel: keys of a split; tile kernel: splits share a row tile's key tiles
   uint64_t wait_limit_ns;
+};
+
+// bf16 keys and values for the tile kernel, [heads of all pages][rows][d]; boxes of box_rows rows x 64 values.
+struct PagedMaps {
+  CUtensorMap k, v;
 };
 
 // A sequence as the kernels use it. Values that the caller's device arrays hold are clamped into the
@@ -128,9 +134,9 @@ __device__ __forceinline__ float ex2_approx(float x) {
 
 // ---- INT8 values in an f16 product: a weight enters as w = p * s_v * c with c a power of two, so that w
 // fits f16 whatever the scales' range (c = 1 / 2^floor(log2 s), s the largest scale seen when c was set:
-// p <= 2^8 by the lazy running max, s_v * c < 2^7 by kScaleGrow, so w < 2^15). f16 keeps 11 bits of a
+// p <= 2^12 by the lazy running max, s_v * c < 2^3 by kScaleGrow, so w < 2^15). f16 keeps 11 bits of a
 // weight where bf16 would keep 8; the sum of the weights takes p itself, in fp32.
-constexpr float kScaleGrow = 128.f;   // s_v * c reaches this: c is set anew and the output so far rescaled
+constexpr float kScaleGrow = 8.f;    // s_v * c reaches this: c is set anew and the output so far rescaled
 __device__ __forceinline__ float scale_norm(float s) {   // 2^-floor(log2 s), both in the normal range
   const int e = min(max(int(__float_as_uint(s) >> 23), 1), 253);
   return __uint_as_float(uint32_t(254 - e) << 23);
@@ -141,7 +147,7 @@ cudaError_t launch_paged_write(const PagedArgs& a, bool int8, const __nv_bfloat1
 cudaError_t launch_paged_read(const PagedArgs& a, bool int8, const int32_t* first, int L, __nv_bfloat16* k_out,
                               __nv_bfloat16* v_out, cudaStream_t st);
 cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st);
-cudaError_t launch_paged_tiles(const PagedArgs& a, bool int8, cudaStream_t st);
+cudaError_t launch_paged_tiles(const PagedArgs& a, const PagedMaps& maps, bool int8, cudaStream_t st);
 cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st);
 
 }  // namespace bsva

@@ -58,14 +58,25 @@ int check_heads(int Hq, int Hkv, long long max_q) {
 // How a call is laid over the GPU. Few rows leave few CTAs, so their keys are split and joined by a second
 // kernel; the number of splits follows from the host bounds alone.
 struct Plan {
+  bool tiles = false;   // tensor-core tiles of 256 rows, or 8 or 16 rows a CTA
   int nsplit = 1, split_keys = 0;
   int cap = 1;   // >= nsplit, and no smaller for more keys: workspaces are sized by it
 };
 
 Plan make_plan(int S, int Hkv, int G, int max_q, int keys) {
   Plan p;
-  const long long rows = (long long)max_q * G, nr = rows <= 8 ? 8 : 16;
-  const long long items = (rows + nr - 1) / nr * Hkv * S;
+  const long long rows = (long long)max_q * G;
+  p.tiles = rows > 16;
+  if (p.tiles) {
+    // 256 rows a CTA and one CTA an SM: splits of at least four key tiles until the SMs are filled
+    const long long items = (rows + 255) / 256 * Hkv * S, most = (keys + 511) / 512;
+    long long n = 148 / items;
+    n = n < most ? n : most;
+    n = n < kMaxSplits ? n : kMaxSplits;
+    p.nsplit = p.cap = int(n < 1 ? 1 : n);
+    return p;
+  }
+  const long long nr = rows <= 8 ? 8 : 16, items = (rows + nr - 1) / nr * Hkv * S;
   const long long want = 148 * 8;
   long long n = (want + items - 1) / items;
   const long long most = (keys + 127) / 128;      // a split has 128 keys at least: two blocks a warp
@@ -106,7 +117,17 @@ int run_paged(PagedArgs& a, bool int8, const Plan& p, const PagedWs& w, void* wo
   a.split_keys = p.split_keys;
   a.part_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
   a.part_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + w.part_ml) : nullptr;
-  cudaError_t e = launch_paged_rows(a, int8, st);
+  PagedMaps maps{};
+  if (p.tiles && !int8) {
+    int rc;
+    a.box_rows = a.page_table && a.page_rows < 128 ? a.page_rows : 128;
+    if ((rc = get_encoder())) return rc;
+    for (int z = 0; z < 2; ++z)
+      if ((rc = encode_map(z ? &maps.v : &maps.k, z ? a.v : a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.d, a.page_rows,
+                           uint64_t(a.n_pages) * a.Hkv, 64, a.box_rows, CU_TENSOR_MAP_SWIZZLE_128B, z ? "v" : "k")))
+        return rc;
+  }
+  cudaError_t e = p.tiles ? launch_paged_tiles(a, maps, int8, st) : launch_paged_rows(a, int8, st);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   if (p.nsplit > 1) {
     e = launch_paged_combine(a, st);

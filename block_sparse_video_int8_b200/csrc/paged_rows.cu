@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   // keys that some row of the tile sees, and this split's part of them (from a multiple of 16)
   const int past = sv.kv - sv.n;
   const int hi_all = a.causal ? min(sv.kv, past + i1 + 1) : sv.kv;
-  const int lo_all = a.window ? max(0, past + i0 - a.window + 1) & ~15 : 0;
+  const int lo_see = a.window ? max(0, past + i0 - a.window + 1) : 0, lo_all = lo_see & ~15;
   const int lo = min((long long)lo_all + (long long)sp * a.split_keys, (long long)INT_MAX - 64);
   const int hi = min((long long)hi_all, (long long)lo + a.split_keys);
 
@@ -133,11 +133,11 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       if constexpr (I8) ks[e] = in ? __ldg(a.k_scale + row + g + 8 * e) * a.scale_log2 : 0.f;
     }
   };
-  auto load_v = [&](int key) {            // zeros behind the last key: what stale rows hold must not reach O
+  auto load_v = [&](int key) {            // zeros where no row sees: what unwritten rows hold must not reach O
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int kk = 2 * t + (e & 1) + 8 * (e >> 1);
-      const bool in = key + kk < hi;
+      const bool in = key + kk < hi && key + kk >= lo_see;
       const char* p = vbase + (row + kk) * (D * EB) + g * VB;
       if constexpr (VB == 8) {
         const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
@@ -152,7 +152,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
     if constexpr (I8) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) vs[e] = key + g + 8 * e < hi ? __ldg(a.v_scale + row + g + 8 * e) : 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const int kk = key + g + 8 * e;
+        vs[e] = kk < hi && kk >= lo_see ? __ldg(a.v_scale + row + g + 8 * e) : 0.f;
+      }
     }
   };
 
@@ -192,8 +195,9 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     load_k(key + STEP);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      x[nt][0] *= f0; x[nt][1] *= f0;
-      x[nt][2] *= f1; x[nt][3] *= f1;
+      // rounded here, not fused with the subtraction of the maximum, which was taken from rounded logits
+      x[nt][0] = __fmul_rn(x[nt][0], f0); x[nt][1] = __fmul_rn(x[nt][1], f0);
+      x[nt][2] = __fmul_rn(x[nt][2], f1); x[nt][3] = __fmul_rn(x[nt][3], f1);
     }
     if (key < full_lo || key + 16 > min(full_hi, hi)) {
 #pragma unroll

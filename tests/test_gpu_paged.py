@@ -225,6 +225,25 @@ def test_longer_chunks(gpu_lib, dtype, n, kv, G, H, d, window):
 
 
 @pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n,page", [(1, 16), (1, 64), (150, 16), (150, 128), (150, 256)])
+def test_tokens_before_the_window_are_gone(gpu_lib, dtype, n, page):
+    window, lens = 70, [(n, 777), (n, 300)]
+    st = Setup(gpu_lib, lens, 2, 64, page, dtype, seed=n + page)
+    table = st.table.copy()
+    for s, (_, kv) in enumerate(lens):
+        first = kv - n - window + 1            # the first token that some row sees
+        for pool, scale in ((st.cache.k, st.cache.k_scale), (st.cache.v, st.cache.v_scale)):
+            t = np.arange(first // page * page, first)
+            if dtype == torch.int8:
+                scale[st.table[s][t // page], :, t % page] = NAN
+            else:
+                pool[st.table[s][t // page], :, t % page] = NAN
+        table[s, :first // page] = -1
+    st.batch.page_table.copy_(torch.from_numpy(table))
+    _attend(st, 4, True, window)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
 @pytest.mark.parametrize("n", [1, 200])
 def test_rows_without_keys(gpu_lib, dtype, n):
     # sequences shorter than their chunk: the first rows see nothing; a sequence without any key
