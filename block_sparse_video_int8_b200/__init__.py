@@ -617,32 +617,46 @@ class KVCache:
 
 
 # ------------------------------------------------------------------------- paged K/V cache, cross attention
-def _on(device, name, *tensors):
-    """The tensors of a call lie on one CUDA device (the library works on the current one)."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+# A decoding step makes these calls once a layer for a few microseconds of GPU work each, so they marshal with as little
+# as they can: one comparison an argument while it is as it should be, messages only when it is not, pointers as plain
+# integers, structs built once.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _token_stride(t, H, d, name):
-    """Elements between the tokens of [T, H, d] whose heads and values are dense."""
+def _stream_of(stream, index: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _dense(t, dtype, shape, index, name) -> int:
+    """The address of a contiguous tensor on device ``index`` (``shape`` None: any)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
+    _need(t, dtype, shape, name)
+    raise ValueError(f"{name} is on {t.device}, the call is on cuda:{index}")
+
+
+def _tokens(t, H, d, index, name) -> int:
+    """Elements between the tokens of bf16 [T, H, d] (H None: any) whose heads and values are dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dim() != 3 or t.shape[2] != d or (H is not None and t.shape[1] != H):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, {H or 'heads'}, {d}]")
-    H = t.shape[1]
-    if t.shape[0] <= 1:
-        if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != d)):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        return H * d
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d) or t.stride(0) < H * d or t.stride(0) % 8:
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        raise ValueError(f"{name} is on {t.device}, the call is on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (H is not None and shape[1] != H):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [T, {H or 'heads'}, {d}]")
+    row = shape[1] * d
+    st, sh, sd = t.stride()
+    if t.numel() and (sd != 1 or (shape[1] > 1 and sh != d) or (shape[0] > 1 and (st < row or st % 8))):
         raise ValueError(f"{name}: strides {t.stride()}; the heads of a token must be contiguous and tokens a multiple "
                          "of 8 elements apart, at least heads * d")
-    return t.stride(0)
+    return st if shape[0] > 1 else row
 
 
 class PagedBatch:
@@ -651,7 +665,7 @@ class PagedBatch:
     ``q_start`` int32 [S+1]: sequence s has new tokens ``q_start[s] .. q_start[s+1]-1`` of the packed tensors;
     ``kv_len`` int32 [S]: its tokens, the new ones included; ``page_table`` int32 [S, max_pages]. ``max_q`` and
     ``max_kv`` are host bounds of new tokens and tokens of a sequence. The tensors are kept and read by every
-    call, so a captured graph replays with what they hold then."""
+    call, so a captured graph replays with what they hold then; other tensors or bounds are another batch."""
 
     def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, max_q: int, max_kv: int):
         _need(kv_len, torch.int32, None, "kv_len")
@@ -662,15 +676,30 @@ class PagedBatch:
         _need(page_table, torch.int32, None, "page_table")
         if page_table.dim() != 2 or page_table.shape[0] != S:
             raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [{S}, max_pages]")
-        _on(kv_len.device, "q_start", q_start)
-        _on(kv_len.device, "page_table", page_table)
-        self.S, self.max_q, self.max_kv = S, int(max_q), int(max_kv)
-        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
-        self.device = kv_len.device
+        for n, t in (("q_start", q_start), ("page_table", page_table)):
+            if t.device != kv_len.device:
+                raise ValueError(f"{n} is on {t.device}, kv_len is on {kv_len.device}")
+        self._of = (S, int(max_q), int(max_kv), q_start, kv_len, page_table)
+        self._index = kv_len.get_device()
+        self._refs: dict = {}
 
-    def _struct(self, T: int) -> PagedBatchStruct:
-        return PagedBatchStruct(self.S, T, self.max_q, self.max_kv, self.page_table.shape[1], self.q_start.data_ptr(),
-                                self.kv_len.data_ptr(), self.page_table.data_ptr())
+    S = property(lambda self: self._of[0])
+    max_q = property(lambda self: self._of[1])
+    max_kv = property(lambda self: self._of[2])
+    q_start = property(lambda self: self._of[3])
+    kv_len = property(lambda self: self._of[4])
+    page_table = property(lambda self: self._of[5])
+
+    def _ref(self, T: int, index: int):
+        """The struct for ``T`` packed rows, by reference."""
+        if index != self._index:
+            raise ValueError(f"batch is on cuda:{self._index}, the call is on cuda:{index}")
+        r = self._refs.get(T)
+        if r is None:
+            S, max_q, max_kv, q_start, kv_len, table = self._of
+            r = self._refs[T] = ctypes.byref(PagedBatchStruct(S, T, max_q, max_kv, table.shape[1], q_start.data_ptr(),
+                                                              kv_len.data_ptr(), table.data_ptr()))
+        return r
 
 
 class PagedKVCache:
@@ -702,72 +731,70 @@ class PagedKVCache:
         if not isinstance(k, torch.Tensor) or k.dim() != 4 or k.dtype not in (torch.int8, torch.bfloat16):
             raise TypeError("k must be an int8 or bf16 tensor [n_pages, H, page_size, d]")
         _need(k, k.dtype, None, "k")
-        _need(v, k.dtype, tuple(k.shape), "v")
+        index = self._index = k.get_device()
+        ptr = [k.data_ptr(), _dense(v, k.dtype, k.shape, index, "v"), None, None]
         if k.dtype == torch.int8:
-            _need(ks, torch.float32, tuple(k.shape[:3]), "k_scale")
-            _need(vs, torch.float32, tuple(k.shape[:3]), "v_scale")
+            ptr[2:] = [_dense(t, torch.float32, k.shape[:3], index, n) for n, t in (("k_scale", ks), ("v_scale", vs))]
         elif ks is not None or vs is not None:
             raise ValueError("bf16 pages have no scales")
-        for n, t in (("v", v), ("k_scale", ks), ("v_scale", vs)):
-            _on(k.device, n, t)
         self.k, self.v, self.k_scale, self.v_scale = k, v, ks, vs
         self.n_pages, self.H, self.page_size, self.d = k.shape
-        self.c = PagedKVStruct(self.n_pages, self.page_size, self.H, self.d, 0 if k.dtype == torch.int8 else 1,
-                               k.data_ptr(), v.data_ptr(), ks.data_ptr() if ks is not None else None,
-                               vs.data_ptr() if vs is not None else None)
+        self._lib = load()
+        self._ref = ctypes.byref(PagedKVStruct(self.n_pages, self.page_size, self.H, self.d,
+                                               0 if k.dtype == torch.int8 else 1, *ptr))
 
     def workspace_bytes(self, batch: PagedBatch, Hq: int, T: int | None = None) -> int:
         """Bytes for calls of ``T`` packed rows (by default S * max_q) and up to ``Hq`` query heads."""
-        b = batch._struct(batch.S * batch.max_q if T is None else T)
-        n = load().bsva_paged_workspace_bytes(ctypes.byref(self.c), ctypes.byref(b), Hq)
+        n = self._lib.bsva_paged_workspace_bytes(self._ref, batch._ref(batch.S * batch.max_q if T is None else T,
+                                                                       self._index), Hq)
         if n == 0:
-            raise BsvaError(1, load().bsva_last_error().decode(errors="replace"))
+            raise BsvaError(1, self._lib.bsva_last_error().decode(errors="replace"))
         return n
 
     def new_workspace(self, batch: PagedBatch, Hq: int, T: int | None = None) -> torch.Tensor:
         return torch.zeros(self.workspace_bytes(batch, Hq, T), dtype=torch.uint8, device=self.k.device)
 
-    def _workspace(self, workspace, need):
-        if workspace is None:
-            return torch.zeros(need, dtype=torch.uint8, device=self.k.device)
-        _need(workspace, torch.uint8, None, "workspace")
-        _on(self.k.device, "workspace", workspace)
-        return workspace
-
     def write(self, k: torch.Tensor, v: torch.Tensor, batch: PagedBatch, workspace=None, stream=None):
         """The batch's new tokens, bf16 [T, H, d], into their pages (C ABI ``bsva_paged_kv_write``); tokens may be
         strided, as slices of a fused projection are."""
-        ks, vs = _token_stride(k, self.H, self.d, "k"), _token_stride(v, self.H, self.d, "v")
-        if v.shape[0] != k.shape[0]:
-            raise ValueError(f"k has {k.shape[0]} tokens, v has {v.shape[0]}")
-        for n, t in (("k", k), ("v", v), ("batch", batch)):
-            _on(self.k.device, n, t)
-        with torch.cuda.device(self.k.device):
-            ws = self._workspace(workspace, 256)
-            b = batch._struct(k.shape[0])
-            _check(load().bsva_paged_kv_write(ctypes.byref(self.c), ctypes.byref(b), _ptr(k), _ptr(v), ks, vs, _ptr(ws),
-                                              ws.numel(), _stream(stream)))
+        index = self._index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.write(k, v, batch, workspace, stream)
+        ks, vs = _tokens(k, self.H, self.d, index, "k"), _tokens(v, self.H, self.d, index, "v")
+        T = k.shape[0]
+        if v.shape[0] != T:
+            raise ValueError(f"k has {T} tokens, v has {v.shape[0]}")
+        ws = torch.zeros(256, dtype=torch.uint8, device=self.k.device) if workspace is None else workspace
+        rc = self._lib.bsva_paged_kv_write(self._ref, batch._ref(T, index), k.data_ptr(), v.data_ptr(), ks, vs,
+                                           _dense(ws, torch.uint8, None, index, "workspace"), ws.numel(),
+                                           _stream_of(stream, index))
+        if rc:
+            _check(rc)
 
     def read(self, batch: PagedBatch, first: torch.Tensor | None = None, length: int | None = None, out=None,
              workspace=None, stream=None):
         """Cached tokens ``first[s]`` (default 0) to the end of each sequence as bf16 (k, v) [S, H, length, d], zeros
         behind them; ``length`` defaults to ``max_kv`` (C ABI ``bsva_paged_kv_read``)."""
+        index = self._index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.read(batch, first, length, out, workspace, stream)
+        S = batch.S
         L = batch.max_kv if length is None else int(length)
-        if first is not None:
-            _need(first, torch.int32, (batch.S,), "first")
-        shape = (batch.S, self.H, L, self.d)
-        for n, t in (("first", first), ("batch", batch)):
-            _on(self.k.device, n, t)
-        with torch.cuda.device(self.k.device):
-            if out is None:
-                out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=self.k.device) for _ in range(2))
-            for n, t in (("k_out", out[0]), ("v_out", out[1])):
-                _need(t, torch.bfloat16, shape, n)
-                _on(self.k.device, n, t)
-            ws = self._workspace(workspace, 256)
-            b = batch._struct(0)
-            _check(load().bsva_paged_kv_read(ctypes.byref(self.c), ctypes.byref(b), _ptr(first), L, _ptr(out[0]),
-                                             _ptr(out[1]), _ptr(ws), ws.numel(), _stream(stream)))
+        shape = (S, self.H, L, self.d)
+        fp = None if first is None else _dense(first, torch.int32, (S,), index, "first")
+        if out is None:
+            dev = self.k.device
+            out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
+        ws = torch.zeros(256, dtype=torch.uint8, device=self.k.device) if workspace is None else workspace
+        rc = self._lib.bsva_paged_kv_read(self._ref, batch._ref(0, index), fp, L,
+                                          _dense(out[0], torch.bfloat16, shape, index, "k_out"),
+                                          _dense(out[1], torch.bfloat16, shape, index, "v_out"),
+                                          _dense(ws, torch.uint8, None, index, "workspace"), ws.numel(),
+                                          _stream_of(stream, index))
+        if rc:
+            _check(rc)
         return out
 
     def attend(self, q: torch.Tensor, batch: PagedBatch, causal: bool = True, window: int = 0,
@@ -775,29 +802,27 @@ class PagedKVCache:
         """Attention of the batch's new tokens, q bf16 [T, Hq, d], over their sequences' cached keys (C ABI
         ``paged_attn_fwd``). Returns ``out`` [T, Hq, d] or ``(out, lse)``; rows behind the last sequence are left as
         they were (``out`` and ``lse`` that the call allocates: zeros)."""
-        qs = _token_stride(q, None, self.d, "q")
+        index = self._index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return self.attend(q, batch, causal, window, softmax_scale, with_lse, workspace, out, lse, stream)
+        qs = _tokens(q, None, self.d, index, "q")
         T, Hq, d = q.shape
-        for n, t in (("q", q), ("batch", batch)):
-            _on(self.k.device, n, t)
-        with torch.cuda.device(self.k.device):
-            if out is None:
-                out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-            if with_lse and lse is None:
-                lse = torch.zeros((T, Hq), dtype=torch.float32, device=q.device)
-            _need(out, torch.bfloat16, (T, Hq, d), "out")
-            _on(self.k.device, "out", out)
-            if lse is not None:
-                _need(lse, torch.float32, (T, Hq), "lse")
-                _on(self.k.device, "lse", lse)
-            b = batch._struct(T)
-            ws = workspace
-            if ws is None:
-                need = load().bsva_paged_workspace_bytes(ctypes.byref(self.c), ctypes.byref(b), Hq)
-                ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
-            ws = self._workspace(ws, 0)
-            _check(load().paged_attn_fwd(ctypes.byref(self.c), ctypes.byref(b), _ptr(q), qs, Hq, int(causal), int(window),
-                                         ctypes.c_float(softmax_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                         _stream(stream)))
+        b = batch._ref(T, index)
+        if out is None:
+            out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        if with_lse and lse is None:
+            lse = torch.zeros((T, Hq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            n = self._lib.bsva_paged_workspace_bytes(self._ref, b, Hq)
+            workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)   # 0: the call below says why
+        rc = self._lib.paged_attn_fwd(self._ref, b, q.data_ptr(), qs, Hq, 1 if causal else 0, window, softmax_scale,
+                                      _dense(out, torch.bfloat16, (T, Hq, d), index, "out"),
+                                      None if lse is None else _dense(lse, torch.float32, (T, Hq), index, "lse"),
+                                      _dense(workspace, torch.uint8, None, index, "workspace"), workspace.numel(),
+                                      _stream_of(stream, index))
+        if rc:
+            _check(rc)
         return (out, lse) if with_lse else out
 
 
@@ -823,22 +848,28 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_len: tor
     """Attention of q bf16 [B, H, Lq, d] to k, v bf16 [B, Hkv, Lk, d], the first ``k_len[b]`` (int32 [B], default Lk)
     keys of each batch entry (C ABI ``cross_attn_fwd``). H is a multiple of Hkv."""
     s, Hkv = _cross_shape(q, k)
-    _need(q, torch.bfloat16, None, "q")
-    _need(k, torch.bfloat16, (s.B, Hkv, s.Lk, s.d), "k")
-    _need(v, torch.bfloat16, (s.B, Hkv, s.Lk, s.d), "v")
-    if k_len is not None:
-        _need(k_len, torch.int32, (s.B,), "k_len")
-    with torch.cuda.device(q.device):
-        out = _out(out, (s.B, s.H, s.Lq, s.d), torch.bfloat16, q.device)
-        if with_lse and lse is None:
-            lse = torch.empty((s.B, s.H, s.Lq), dtype=torch.float32, device=q.device)
-        if lse is not None:
-            _need(lse, torch.float32, (s.B, s.H, s.Lq), "lse")
-        if workspace is None:
-            workspace = new_cross_attn_workspace(q, k)
-        _need(workspace, torch.uint8, None, "workspace")
-        for n, t in (("k", k), ("v", v), ("k_len", k_len), ("out", out), ("lse", lse), ("workspace", workspace)):
-            _on(q.device, n, t)
-        _check(load().cross_attn_fwd(s, Hkv, _ptr(q), _ptr(k), _ptr(v), _ptr(k_len), ctypes.c_float(softmax_scale),
-                                     _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    index = q.get_device()
+    if index < 0:
+        _need(q, torch.bfloat16, None, "q")
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return cross_attn_fwd(q, k, v, k_len, softmax_scale, with_lse, workspace, out, lse, stream)
+    qp = _dense(q, torch.bfloat16, None, index, "q")
+    kv = (s.B, Hkv, s.Lk, s.d)
+    kp, vp = _dense(k, torch.bfloat16, kv, index, "k"), _dense(v, torch.bfloat16, kv, index, "v")
+    lp = None if k_len is None else _dense(k_len, torch.int32, (s.B,), index, "k_len")
+    rows = (s.B, s.H, s.Lq)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if with_lse and lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = new_cross_attn_workspace(q, k)
+    lib = load()
+    rc = lib.cross_attn_fwd(s, Hkv, qp, kp, vp, lp, softmax_scale, _dense(out, torch.bfloat16, q.shape, index, "out"),
+                            None if lse is None else _dense(lse, torch.float32, rows, index, "lse"),
+                            _dense(workspace, torch.uint8, None, index, "workspace"), workspace.numel(),
+                            _stream_of(stream, index))
+    if rc:
+        _check(rc)
     return (out, lse) if with_lse else out

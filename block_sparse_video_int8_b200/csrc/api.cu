@@ -4,6 +4,7 @@
 // bsva_check_status, whose job is to synchronise), and none falls back to
 // another path: a bad argument or an unsupported device returns an error code
 // and leaves every output untouched.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -44,6 +45,8 @@ int check_device() {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  static std::atomic<uint64_t> known{0};   // bit d: device d was found to be sm_100
+  if (dev < 64 && (known.load(std::memory_order_relaxed) >> dev & 1)) return BSVA_OK;
   int major = 0, minor = 0;
   e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
@@ -51,6 +54,7 @@ int check_device() {
   if (major != 10 || minor != 0)
     return fail(BSVA_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a (B200) only", dev,
                 major, minor);
+  if (dev < 64) known.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   return BSVA_OK;
 }
 

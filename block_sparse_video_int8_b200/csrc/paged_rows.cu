@@ -346,6 +346,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
 template <int D>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
   constexpr int LPR = D / 4;
+  // launched while the kernel that writes the parts still runs: from here on its results are there
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long x = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // (token, head) of the sequence
   const int c = threadIdx.x % LPR;
   const int s = blockIdx.y, Hq = a.Hkv * a.G;
@@ -391,10 +393,18 @@ cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st) {
 
 cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st) {
   const long long rows = (long long)a.max_q * a.Hkv * a.G, rpb = 256 / (a.d / 4);
-  const dim3 grid(unsigned((rows + rpb - 1) / rpb), a.S);
-  if (a.d == 128) paged_combine_kernel<128><<<grid, 256, 0, st>>>(a);
-  else paged_combine_kernel<64><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  // the launch overlaps the end of the kernel before it (the parts' writer); the device waits for that one itself
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned((rows + rpb - 1) / rpb), a.S);
+  cfg.blockDim = 256;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return a.d == 128 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, a)
+                    : cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, a);
 }
 
 }  // namespace bsva
