@@ -8,15 +8,18 @@
 // r % G. One CTA = (row tile of 8 * NT rows, split of the keys, key head, sequence); its four warps take
 // 16-key blocks in turn, each with its own running maximum, sum and output, and join at the end.
 // Such calls are bound by reading the codes (an INT8 key head's token is 2 d + 8 bytes for 4 d flops a
-// row), so codes go from global memory straight into registers, in an order that is already that of the
-// tensor-core fragments, and both products have the keys' data on the 16-row side, so that 8 rows waste
-// nothing:
-//   S^T [16 keys x 8 rows] += K [16 x 16] . Q^T [16 x 8]        (bf16; INT8 codes widened, exact)
+// row), and what bounds the reading is how many bytes are on their way: each warp keeps a ring of 16-key
+// blocks of its own in shared memory, filled by cp.async two or three blocks ahead with no registers held
+// and no barrier but the warp's, and both products have the keys' data on the 16-row side, so that 8 rows
+// waste nothing:
+//   S^T [16 keys x 8 rows] += K [16 x 16] . Q^T [16 x 8]        (f16 for INT8 codes, widened exactly; bf16)
 //   O^T [16 d   x 8 rows] += V^T [16 x 16 keys] . P^T [16 x 8]  (f16 for INT8 codes, bf16 for bf16 values)
 // A product's inner index may run in any order that both operands share, and so may the d index of O:
-//   lane (g = lane / 4, t = lane % 4) reads 16-byte pieces of key rows g and g + 8 and takes four
-//   consecutive d values a step; of V it reads d values [g d/8, (g + 1) d/8) of keys 2t, 2t+1, 2t+8, 2t+9.
-// The loads of the next block's K are issued as soon as this block's codes are consumed, then V's.
+//   lane (g = lane / 4, t = lane % 4) reads 16-byte pieces of K's tile rows g and g + 8 and takes four
+//   consecutive d values a step; of V it reads 1/8 of the d values of tile rows 2t, 2t+1, 2t+8, 2t+9.
+// Tile row g is key g or, odd, key g ^ 4, and pieces of a row are stored exclusive-or its number: eight
+// lanes that read together then meet eight different banks, for K and for V.
+
 #include <climits>
 
 #include "paged.cuh"
@@ -45,6 +48,27 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool in) {   // zeros where !in
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+
+// A warp's ring: blocks of 16 keys, K, V and (INT8) the scales.
+template <int D, bool I8>
+constexpr int kStageBytes = 32 * D * (I8 ? 1 : 2) + (I8 ? 128 : 0);
+template <int D, bool I8>
+constexpr int kStages = D == 128 && !I8 ? 3 : 4;
+template <int D, bool I8, int NT>
+constexpr int kRowSmem() {
+  constexpr int ring = 4 * kStages<D, I8> * kStageBytes<D, I8>, join = 4 * 8 * NT * (D + 4) * 4;
+  return ring > join ? ring : join;
 }
 
 template <int D, bool I8, int NT>
@@ -86,14 +110,19 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   const int full_lo = a.window ? max(0, past + i1 - a.window + 1) : 0;
   const int full_hi = a.causal ? min(sv.kv, past + i0 + 1) : sv.kv;
 
-  // q as the B operand: lane (g, t) holds row 8 nt + g, the d values its key pieces have
+  // q as the B operand: lane (g, t) holds row 8 nt + g, the d values its key pieces have. With INT8 codes it enters as
+  // f16, whose codes widen in fewer instructions than bf16's: a row times 2^-x with its largest value in [2^14, 2^15).
+  // That is exact but for values below 2^-29 of the row's largest, which lose at most 2^-39 of it. qf: 2^x of the
+  // rows that are this lane's columns.
   uint32_t bq[NT][KS][2];
+  float qf[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = rb + 8 * nt + g;
     const bool have = r < R;
     const __nv_bfloat16* qp = a.q + (long long)s * a.q_seq + (long long)(sv.q0 + (have ? r / a.G : 0)) * a.q_tok +
                               (long long)(h * a.G + (have ? r % a.G : 0)) * a.q_head;
+    float top = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
       // four consecutive d values: INT8 pieces hold 16 of them, bf16 pieces 8
@@ -101,6 +130,25 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       const uint2 w = have ? __ldg(reinterpret_cast<const uint2*>(qp + d0)) : make_uint2(0, 0);
       bq[nt][kk][0] = I8 ? __byte_perm(w.x, w.y, 0x5410) : w.x;   // INT8: (d0, d0+2), (d0+1, d0+3)
       bq[nt][kk][1] = I8 ? __byte_perm(w.x, w.y, 0x7632) : w.y;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(bq[nt][kk][e] << 16)),
+                               fabsf(__uint_as_float(bq[nt][kk][e] & 0xffff0000u))));
+    }
+    qf[nt][0] = qf[nt][1] = 1.f;
+    if constexpr (I8) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int x = min(max(int(__float_as_uint(top) >> 23), 15), 240) - 14;      // biased exponent of 2^x
+      const float down = __uint_as_float(uint32_t(254 - x) << 23), up = __uint_as_float(uint32_t(x) << 23);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          bq[nt][kk][e] = pack_f16x2(__uint_as_float(bq[nt][kk][e] << 16) * down,
+                                     __uint_as_float(bq[nt][kk][e] & 0xffff0000u) * down);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qf[nt][e] = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
     }
   }
 
@@ -116,57 +164,85 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   }
   float cn = 0.f;                         // INT8: the scales' power of two (0: not set yet)
 
-  uint4 kr[2][KL];
-  uint32_t vr[4][VW];
-  float ks[2], vs[2];
+  extern __shared__ __align__(128) unsigned char smem_rows[];
+  constexpr int RB = D * EB, CPR = RB / 16;             // bytes and 16-byte pieces of a cached row
+  constexpr int STAGE = kStageBytes<D, I8>, NS = kStages<D, I8>;
+  unsigned char* ring = smem_rows + warp * (NS * STAGE);
+  // piece c of row r of a block, within a stage's K or V
+  auto piece = [](int r, int c) { return r * RB + (CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) * 16; };
+  const int kg = g & 1 ? g ^ 4 : g;       // key of tile row g
   const char* kbase = static_cast<const char*>(a.k);
   const char* vbase = static_cast<const char*>(a.v);
-  size_t row = 0;                         // first row of the block whose loads come next
-  auto locate = [&](int key) { row = key < hi ? kv_row(a, page_of(a, s, key), h, key) : 0; };
-  auto load_k = [&](int key) {
+  // Block at `key` into stage st; rows that no row of the tile sees become zeros: what unwritten memory holds must
+  // not reach O. Rows of a block lie in one page (pages hold a multiple of 16 tokens), found a block ahead.
+  int page = 0;
+  auto find = [&](int key) { page = key < hi ? page_of(a, s, key) : 0; };
+  // where this lane's pieces go: x = lane + 32 i is row x / CPR, piece x % CPR; a step of i moves 32 / CPR rows, and the
+  // swizzle repeats every 8 rows
+  constexpr int NI = CPR / 2, RI = 32 / CPR, PER = RI >= 8 ? 1 : 8 / RI;
+  uint32_t to[PER];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const bool in = key + g + 8 * e < hi;
-      const uint4* p = reinterpret_cast<const uint4*>(kbase + (row + g + 8 * e) * (D * EB)) + t;
+  for (int i = 0; i < PER; ++i) to[i] = smem_u32(ring) + piece(lane / CPR + i * RI, lane % CPR);
+  const uint32_t to_scale = smem_u32(ring) + 32 * RB + lane * 4;
+  const float* scales = I8 ? (lane < 16 ? a.k_scale : a.v_scale) + (lane & 15) : nullptr;
+  auto issue = [&](int st, int key) {
+    if (key < hi) {
+      const size_t row = kv_row(a, page, h, key);
+      const bool whole = key >= lo_see && key + 16 <= hi;
+      const char* kp = kbase + row * RB + lane * 16;
+      const char* vp = vbase + row * RB + lane * 16;
+      if (whole) {
 #pragma unroll
-      for (int c = 0; c < KL; ++c) kr[e][c] = in ? __ldg(p + 4 * c) : make_uint4(0, 0, 0, 0);
-      if constexpr (I8) ks[e] = in ? __ldg(a.k_scale + row + g + 8 * e) * a.scale_log2 : 0.f;
-    }
-  };
-  auto load_v = [&](int key) {            // zeros where no row sees: what unwritten rows hold must not reach O
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int kk = 2 * t + (e & 1) + 8 * (e >> 1);
-      const bool in = key + kk < hi && key + kk >= lo_see;
-      const char* p = vbase + (row + kk) * (D * EB) + g * VB;
-      if constexpr (VB == 8) {
-        const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
-        vr[e][0] = x.x; vr[e][1] = x.y;
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t d = to[i % PER] + st * STAGE + (i / PER) * (PER * RI * RB);
+          cp_async<16>(d, kp + i * 512, true);
+          cp_async<16>(d + 16 * RB, vp + i * 512, true);
+        }
+        if constexpr (I8) cp_async<4>(to_scale + st * STAGE, scales + row, true);
       } else {
 #pragma unroll
-        for (int c = 0; c < VB / 16; ++c) {
-          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(p) + c) : make_uint4(0, 0, 0, 0);
-          vr[e][4 * c] = x.x; vr[e][4 * c + 1] = x.y; vr[e][4 * c + 2] = x.z; vr[e][4 * c + 3] = x.w;
+        for (int i = 0; i < NI; ++i) {
+          const int r = key + lane / CPR + i * RI;
+          const bool in = r < hi && r >= lo_see;
+          const uint32_t d = to[i % PER] + st * STAGE + (i / PER) * (PER * RI * RB);
+          cp_async<16>(d, in ? kp + i * 512 : kbase, in);
+          cp_async<16>(d + 16 * RB, in ? vp + i * 512 : vbase, in);
+        }
+        if constexpr (I8) {               // 16 scales of K, 16 of V
+          const int r = key + (lane & 15);
+          const bool in = r < hi && r >= lo_see;
+          cp_async<4>(to_scale + st * STAGE, in ? scales + row : a.k_scale, in);
         }
       }
     }
-    if constexpr (I8) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int kk = key + g + 8 * e;
-        vs[e] = kk < hi && kk >= lo_see ? __ldg(a.v_scale + row + g + 8 * e) : 0.f;
-      }
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   constexpr int STEP = 16 * (kRowThreads / 32);
   int key = lo + 16 * warp;
-  if (key < hi) {
-    locate(key);
-    load_k(key);
-    load_v(key);
+  find(key);
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) {
+    issue(st, key + st * STEP);
+    find(key + (st + 1) * STEP);
   }
-  for (; key < hi; key += STEP) {
+  for (int st = 0; key < hi; key += STEP, st = st + 1 == NS ? 0 : st + 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+    __syncwarp();                         // every lane's part of this block is in, and the last block is done with
+    issue(st == 0 ? NS - 1 : st - 1, key + (NS - 1) * STEP);
+    find(key + NS * STEP);
+    const unsigned char* stage = ring + st * STAGE;
+    uint4 kr[2][KL];
+    float ks[2], vs[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int c = 0; c < KL; ++c) kr[e][c] = *reinterpret_cast<const uint4*>(stage + piece(kg + 8 * e, t + 4 * c));
+      if constexpr (I8) {
+        ks[e] = reinterpret_cast<const float*>(stage + 32 * RB)[kg + 8 * e] * a.scale_log2;
+        vs[e] = reinterpret_cast<const float*>(stage + 32 * RB)[16 + kg + 8 * e];
+      }
+    }
     // ---- logits of 16 keys, in log2 units: lane holds keys g (e = 0, 1) and g + 8 (e = 2, 3)
     float x[NT][4];
 #pragma unroll
@@ -179,8 +255,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       if constexpr (I8) {
         const uint32_t* w0 = &kr[0][kk / 4].x + kk % 4;
         const uint32_t* w1 = &kr[1][kk / 4].x + kk % 4;
-        widen_bf16(*w0, a0, a2);
-        widen_bf16(*w1, a1, a3);
+        widen_f16(*w0, a0, a2);
+        widen_f16(*w1, a1, a3);
       } else {
         const uint32_t* w0 = &kr[0][kk / 2].x + 2 * (kk % 2);
         const uint32_t* w1 = &kr[1][kk / 2].x + 2 * (kk % 2);
@@ -188,23 +264,21 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
         a1 = w1[0]; a3 = w1[1];
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_16x8x16<false>(x[nt], a0, a1, a2, a3, bq[nt][kk][0], bq[nt][kk][1]);
+      for (int nt = 0; nt < NT; ++nt) mma_16x8x16<I8>(x[nt], a0, a1, a2, a3, bq[nt][kk][0], bq[nt][kk][1]);
     }
     const float f0 = I8 ? ks[0] : a.scale_log2, f1 = I8 ? ks[1] : a.scale_log2;
-    locate(key + STEP);
-    load_k(key + STEP);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // rounded here, not fused with the subtraction of the maximum, which was taken from rounded logits
-      x[nt][0] = __fmul_rn(x[nt][0], f0); x[nt][1] = __fmul_rn(x[nt][1], f0);
-      x[nt][2] = __fmul_rn(x[nt][2], f1); x[nt][3] = __fmul_rn(x[nt][3], f1);
+      x[nt][0] = __fmul_rn(x[nt][0] * qf[nt][0], f0); x[nt][1] = __fmul_rn(x[nt][1] * qf[nt][1], f0);
+      x[nt][2] = __fmul_rn(x[nt][2] * qf[nt][0], f1); x[nt][3] = __fmul_rn(x[nt][3] * qf[nt][1], f1);
     }
     if (key < full_lo || key + 16 > min(full_hi, hi)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int kk = key + g + 8 * (e >> 1);
+          const int kk = key + kg + 8 * (e >> 1);
           if (kk >= hi || kk < see_lo[nt][e & 1] || kk > see_hi[nt][e & 1]) x[nt][e] = -INFINITY;
         }
     }
@@ -236,8 +310,9 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
     float c0 = 1.f, c1 = 1.f;             // INT8: weight of a key's codes, s_v * cn
     if constexpr (I8) {
-      const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1]))));
-      if (top * cn >= kScaleGrow || (cn == 0.f && top > 0.f)) {
+      const float mine = fmaxf(vs[0], vs[1]);
+      if (__any_sync(0xffffffffu, mine * cn >= kScaleGrow || (cn == 0.f && mine > 0.f))) {
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
         const float c = scale_norm(top), f = cn == 0.f ? 1.f : c / cn;
         cn = c;
 #pragma unroll
@@ -264,7 +339,23 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       bp[nt][0] = transpose_8x8(I8 ? pack_f16x2(p[0] * c0, p[1] * c0) : pack_bf16x2(p[0], p[1]));
       bp[nt][1] = transpose_8x8(I8 ? pack_f16x2(p[2] * c1, p[3] * c1) : pack_bf16x2(p[2], p[3]));
     }
-    // ---- O^T: word w of the lane's V pieces gives d values in pairs, keys (2t, 2t+1) and (2t+8, 2t+9)
+    // ---- O^T: word w of the lane's V pieces gives d values in pairs, tile rows (2t, 2t+1) and (2t+8, 2t+9)
+    uint32_t vr[4][VW];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = (e & 1 ? (2 * t + 1) ^ 4 : 2 * t) + 8 * (e >> 1);
+      const unsigned char* vst = stage + 16 * RB;
+      if constexpr (VB == 8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(vst + piece(r, g >> 1) + (g & 1) * 8);
+        vr[e][0] = x.x; vr[e][1] = x.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < VB / 16; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vst + piece(r, g + 8 * c));
+          vr[e][4 * c] = x.x; vr[e][4 * c + 1] = x.y; vr[e][4 * c + 2] = x.z; vr[e][4 * c + 3] = x.w;
+        }
+      }
+    }
 #pragma unroll
     for (int w = 0; w < VW; ++w) {
       const uint32_t a_lo = __byte_perm(vr[0][w], vr[1][w], 0x5410), a_hi = __byte_perm(vr[0][w], vr[1][w], 0x7632);
@@ -284,13 +375,14 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
         for (int nt = 0; nt < NT; ++nt) mma_16x8x16<false>(o[nt][w], a_lo, a_hi, b_lo, b_hi, bp[nt][0], bp[nt][1]);
       }
     }
-    load_v(key + STEP);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 
   // ---- join the four warps: each leaves its maximum, sum and output (over cn) in shared memory
   constexpr int W = kRowThreads / 32, NR = 8 * NT;
   __shared__ float s_m[W][NR], s_l[W][NR];
-  __shared__ __align__(16) float s_o[W][NR][D + 4];
+  float (*s_o)[NR][D + 4] = reinterpret_cast<float (*)[NR][D + 4]>(smem_rows);   // over the rings, which are through
+  __syncthreads();
   const float inv_c = I8 && cn != 0.f ? 1.f / cn : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -305,9 +397,12 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
         s_l[warp][r] = ls;
       }
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {      // lane's d values: g * D/8 + 2j, + 1
-        s_o[warp][r][g * (D / 8) + 2 * j] = o[nt][j][e] * inv_c;
-        s_o[warp][r][g * (D / 8) + 2 * j + 1] = o[nt][j][e + 2] * inv_c;
+      for (int j = 0; j < MT; ++j) {
+        // lane's d values: of each of its pieces, 16 bytes of codes or values, 8 for INT8 rows of 64
+        constexpr int PV = VB < 16 ? VB : 16 / EB;
+        const int d0 = (2 * j / PV) * 8 * PV + g * PV + 2 * j % PV;
+        s_o[warp][r][d0] = o[nt][j][e] * inv_c;
+        s_o[warp][r][d0 + 1] = o[nt][j][e + 2] * inv_c;
       }
     }
   __syncthreads();
@@ -380,15 +475,21 @@ cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st) {
   const long long rows = (long long)a.max_q * a.G;
   const int nr = rows <= 8 ? 8 : 16;
   const dim3 grid(unsigned((rows + nr - 1) / nr * a.nsplit), a.Hkv, a.S);
-  auto go = [&](auto f) { f<<<grid, kRowThreads, 0, st>>>(a); };
-#define BSVA_ROWS(D, I8) nr == 8 ? go(paged_rows_kernel<D, I8, 1>) : go(paged_rows_kernel<D, I8, 2>)
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto f, int smem) {
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) f<<<grid, kRowThreads, smem, st>>>(a);
+  };
+#define BSVA_ROWS(D, I8)                                              \
+  nr == 8 ? go(paged_rows_kernel<D, I8, 1>, kRowSmem<D, I8, 1>())     \
+          : go(paged_rows_kernel<D, I8, 2>, kRowSmem<D, I8, 2>())
   if (a.d == 128) {
     if (int8) BSVA_ROWS(128, true); else BSVA_ROWS(128, false);
   } else {
     if (int8) BSVA_ROWS(64, true); else BSVA_ROWS(64, false);
   }
 #undef BSVA_ROWS
-  return cudaGetLastError();
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st) {
