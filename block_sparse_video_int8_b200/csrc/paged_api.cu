@@ -77,10 +77,15 @@ Plan make_plan(int S, int Hkv, int G, int max_q, int keys) {
     return p;
   }
   const long long nr = rows <= 8 ? 8 : 16, items = (rows + nr - 1) / nr * Hkv * S;
-  const long long want = 148 * 8;
-  long long n = (want + items - 1) / items;
-  const long long most = (keys + 127) / 128;      // a split has 128 keys at least: two blocks a warp
-  n = n < most ? n : most;
+  // Three CTAs an SM run at once. Splits of 128 keys (two blocks a warp) until they are filled once, of 512 keys until
+  // four times: short ends and unequal sequences then leave few SMs idle, and joining costs little beside 512 keys.
+  // (One, four, eight times, us: 2 x 131000 keys 550, 433, 443; 16 sequences of up to 1500 keys 21, 24.6, 26.7.)
+  auto splits = [&](long long ctas, long long least) {
+    const long long want = (ctas + items - 1) / items, most = (keys + least - 1) / least;
+    return want < most ? want : most;
+  };
+  long long n = splits(148 * 3, 128), n4 = splits(148 * 12, 512);
+  n = n > n4 ? n : n4;
   n = n < kMaxSplits ? n : kMaxSplits;
   n = n < 1 ? 1 : n;
   p.cap = int(n);

@@ -110,48 +110,6 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   const int full_lo = a.window ? max(0, past + i1 - a.window + 1) : 0;
   const int full_hi = a.causal ? min(sv.kv, past + i0 + 1) : sv.kv;
 
-  // q as the B operand: lane (g, t) holds row 8 nt + g, the d values its key pieces have. With INT8 codes it enters as
-  // f16, whose codes widen in fewer instructions than bf16's: a row times 2^-x with its largest value in [2^14, 2^15).
-  // That is exact but for values below 2^-29 of the row's largest, which lose at most 2^-39 of it. qf: 2^x of the
-  // rows that are this lane's columns.
-  uint32_t bq[NT][KS][2];
-  float qf[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = rb + 8 * nt + g;
-    const bool have = r < R;
-    const __nv_bfloat16* qp = a.q + (long long)s * a.q_seq + (long long)(sv.q0 + (have ? r / a.G : 0)) * a.q_tok +
-                              (long long)(h * a.G + (have ? r % a.G : 0)) * a.q_head;
-    float top = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-      // four consecutive d values: INT8 pieces hold 16 of them, bf16 pieces 8
-      const int d0 = I8 ? (kk / 4) * 64 + 16 * t + 4 * (kk % 4) : (kk / 2) * 32 + 8 * t + 4 * (kk % 2);
-      const uint2 w = have ? __ldg(reinterpret_cast<const uint2*>(qp + d0)) : make_uint2(0, 0);
-      bq[nt][kk][0] = I8 ? __byte_perm(w.x, w.y, 0x5410) : w.x;   // INT8: (d0, d0+2), (d0+1, d0+3)
-      bq[nt][kk][1] = I8 ? __byte_perm(w.x, w.y, 0x7632) : w.y;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(bq[nt][kk][e] << 16)),
-                               fabsf(__uint_as_float(bq[nt][kk][e] & 0xffff0000u))));
-    }
-    qf[nt][0] = qf[nt][1] = 1.f;
-    if constexpr (I8) {
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int x = min(max(int(__float_as_uint(top) >> 23), 15), 240) - 14;      // biased exponent of 2^x
-      const float down = __uint_as_float(uint32_t(254 - x) << 23), up = __uint_as_float(uint32_t(x) << 23);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          bq[nt][kk][e] = pack_f16x2(__uint_as_float(bq[nt][kk][e] << 16) * down,
-                                     __uint_as_float(bq[nt][kk][e] & 0xffff0000u) * down);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) qf[nt][e] = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
-    }
-  }
-
   float m[NT][2], l[NT][2], o[NT][MT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -226,6 +184,48 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     issue(st, key + st * STEP);
     find(key + (st + 1) * STEP);
   }
+  // q as the B operand: lane (g, t) holds row 8 nt + g, the d values its key pieces have. With INT8 codes it enters as
+  // f16, whose codes widen in fewer instructions than bf16's: a row times 2^-x with its largest value in [2^14, 2^15).
+  // That is exact but for values below 2^-29 of the row's largest, which lose at most 2^-39 of it. qf: 2^x of the
+  // rows that are this lane's columns.
+  uint32_t bq[NT][KS][2];
+  float qf[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = rb + 8 * nt + g;
+    const bool have = r < R;
+    const __nv_bfloat16* qp = a.q + (long long)s * a.q_seq + (long long)(sv.q0 + (have ? r / a.G : 0)) * a.q_tok +
+                              (long long)(h * a.G + (have ? r % a.G : 0)) * a.q_head;
+    float top = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+      // four consecutive d values: INT8 pieces hold 16 of them, bf16 pieces 8
+      const int d0 = I8 ? (kk / 4) * 64 + 16 * t + 4 * (kk % 4) : (kk / 2) * 32 + 8 * t + 4 * (kk % 2);
+      const uint2 w = have ? __ldg(reinterpret_cast<const uint2*>(qp + d0)) : make_uint2(0, 0);
+      bq[nt][kk][0] = I8 ? __byte_perm(w.x, w.y, 0x5410) : w.x;   // INT8: (d0, d0+2), (d0+1, d0+3)
+      bq[nt][kk][1] = I8 ? __byte_perm(w.x, w.y, 0x7632) : w.y;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(bq[nt][kk][e] << 16)),
+                               fabsf(__uint_as_float(bq[nt][kk][e] & 0xffff0000u))));
+    }
+    qf[nt][0] = qf[nt][1] = 1.f;
+    if constexpr (I8) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int x = min(max(int(__float_as_uint(top) >> 23), 15), 240) - 14;      // biased exponent of 2^x
+      const float down = __uint_as_float(uint32_t(254 - x) << 23), up = __uint_as_float(uint32_t(x) << 23);
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          bq[nt][kk][e] = pack_f16x2(__uint_as_float(bq[nt][kk][e] << 16) * down,
+                                     __uint_as_float(bq[nt][kk][e] & 0xffff0000u) * down);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qf[nt][e] = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
+    }
+  }
+
   for (int st = 0; key < hi; key += STEP, st = st + 1 == NS ? 0 : st + 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
     __syncwarp();                         // every lane's part of this block is in, and the last block is done with
