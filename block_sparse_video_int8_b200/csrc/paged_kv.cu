@@ -16,85 +16,96 @@ namespace bsva {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kWriteRows = 4;   // rows a thread has in flight
+constexpr int kWriteRows = 2;   // rows of K and of V that a thread has in flight
 
-// One CTA per (block of rows of a sequence's new tokens, K or V, sequence); rows are (token, head) pairs,
-// head fastest, as the source has them.
+// Codes of 8 bf16 values (w) of a row with scale sc, rcp = fl(1 / sc) or 0: the fast step of quant.cuh in pairs.
+__device__ __forceinline__ uint2 quant8(const uint32_t (&w)[4], float sc, float rcp) {
+  const float2 rc = make_float2(rcp, rcp), mg = make_float2(kMagic, kMagic), nmg = make_float2(-kMagic, -kMagic),
+               n1 = make_float2(-1.f, -1.f);
+  float2 t[4];
+  float dm = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 q = __fmul2_rn(make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), rc);
+    t[e] = __fadd2_rn(q, mg);
+    const float2 d = __ffma2_rn(__fadd2_rn(t[e], nmg), n1, q);   // exact: how far q is from its integer
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(dm) : "f"(dm), "f"(d.x), "f"(d.y));
+  }
+  // near a half-integer, or a scale below 2^-120 (its reciprocal could overflow): the IEEE division
+  if (dm >= kBand || (sc > 0.f && rcp == 0.f)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      t[e] = make_float2(quant_exact(__uint_as_float(w[e] << 16), sc), quant_exact(__uint_as_float(w[e] & 0xFFFF0000u), sc));
+  }
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = __byte_perm(__float_as_uint(t[e].x), __float_as_uint(t[e].y), 0x0040);
+  return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
+}
+
+// One CTA per (block of 2^shift new tokens, heads that fill its rows up, sequence): a row slot's low bits are the
+// token, so that long chunks write whole runs of a head's page and single tokens fill a CTA with their heads, both
+// without a division. A thread takes kWriteRows rows of K and the same of V.
 template <int D, bool I8>
 __global__ void __launch_bounds__(kKvThreads) paged_write_kernel(const PagedArgs a, const __nv_bfloat16* __restrict__ k,
                                                                  const __nv_bfloat16* __restrict__ v,
-                                                                 long long k_stride, long long v_stride) {
+                                                                 long long k_stride, long long v_stride, int shift) {
   constexpr int LPR = D / 8;                    // lanes of a row
   constexpr int RPP = kKvThreads / LPR;         // rows a pass
+  constexpr int N = 2 * kWriteRows;             // K rows, then V rows
   const int s = blockIdx.z;
-  const bool isV = blockIdx.y == 1;
   const SeqView sv = seq_view(a, s);
-  const long long rows = (long long)sv.n * a.Hkv;
-  const long long row0 = (long long)blockIdx.x * (RPP * kWriteRows) + threadIdx.x / LPR;
+  if (int(blockIdx.x << shift) >= sv.n) return;
   const int c = threadIdx.x % LPR;
-  const __nv_bfloat16* src = isV ? v : k;
-  const long long stride = isV ? v_stride : k_stride;
-
-  uint4 x[kWriteRows];
+  uint4 x[N];
   long long dst[kWriteRows];                    // destination row, or -1
 #pragma unroll
   for (int u = 0; u < kWriteRows; ++u) {
-    const long long r = row0 + (long long)u * RPP;
-    x[u] = make_uint4(0, 0, 0, 0);
+    const int slot = threadIdx.x / LPR + u * RPP;
+    const int i = (blockIdx.x << shift) + (slot & ((1 << shift) - 1));
+    const int h = blockIdx.y * ((RPP * kWriteRows) >> shift) + (slot >> shift);
+    x[u] = x[u + kWriteRows] = make_uint4(0, 0, 0, 0);
     dst[u] = -1;
-    if (r < rows) {
-      const int i = int(r / a.Hkv), h = int(r % a.Hkv);
-      const int pos = sv.kv - sv.n + i;         // negative where kv_len is smaller than the chunk: not written
-      if (pos >= 0) {
-        const int page = __ldg(a.page_table + size_t(s) * a.max_pages + (pos >> a.page_shift));
-        if (unsigned(page) < unsigned(a.n_pages)) {
-          dst[u] = (long long)kv_row(a, page, h, pos);
-          x[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(sv.q0 + i) * stride + (long long)h * D) + c);
-        } else {
-          atomicOr(a.status, kStatusBounds);
-        }
-      } else {
-        atomicOr(a.status, kStatusBounds);
-      }
+    if (i < sv.n && h < a.Hkv) {
+      const long long tok = sv.q0 + i;
+      x[u] = __ldg(reinterpret_cast<const uint4*>(k + tok * k_stride + h * D) + c);
+      x[u + kWriteRows] = __ldg(reinterpret_cast<const uint4*>(v + tok * v_stride + h * D) + c);
+      // a position before the sequence (kv_len smaller than the chunk) or a page outside the cache: not written
+      const int pos = sv.kv - sv.n + i;
+      int page = -1;
+      if (pos >= 0) page = __ldg(a.page_table + size_t(s) * a.max_pages + (pos >> a.page_shift));
+      if (unsigned(page) < unsigned(a.n_pages)) dst[u] = (long long)kv_row(a, page, h, pos);
+      else atomicOr(a.status, kStatusBounds);
     }
   }
+  char* kd = static_cast<char*>(const_cast<void*>(a.k));
+  char* vd = static_cast<char*>(const_cast<void*>(a.v));
   if constexpr (!I8) {
-    uint4* out = reinterpret_cast<uint4*>(const_cast<void*>(isV ? a.v : a.k));
 #pragma unroll
-    for (int u = 0; u < kWriteRows; ++u)
-      if (dst[u] >= 0) out[dst[u] * LPR + c] = x[u];
+    for (int u = 0; u < N; ++u)
+      if (dst[u % kWriteRows] >= 0)
+        reinterpret_cast<uint4*>(u < kWriteRows ? kd : vd)[dst[u % kWriteRows] * LPR + c] = x[u];
   } else {
-    uint2* out = reinterpret_cast<uint2*>(const_cast<void*>(isV ? a.v : a.k));
-    float* scale = const_cast<float*>(isV ? a.v_scale : a.k_scale);
+    float m[N];
 #pragma unroll
-    for (int u = 0; u < kWriteRows; ++u) {
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      float m = bmax_fold(bmax_abs(bmax_abs(w[0], w[1]), bmax_abs(w[2], w[3])));
+    for (int u = 0; u < N; ++u) {
+      uint32_t p = bmax_abs(bmax_abs(x[u].x, x[u].y), bmax_abs(x[u].z, x[u].w));
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float sc = __fdiv_rn(m, 127.0f);
-      // below 2^-120 the reciprocal could overflow: those rows take the IEEE division
-      const bool slow = sc > 0.f && sc < 0x1p-120f;
-      const float rcp = sc >= 0x1p-120f ? __frcp_rn(sc) : 0.f;
-      float t[8], dm = 0.f;
+      for (int o = LPR / 2; o > 0; o >>= 1) p = bmax_abs(p, __shfl_xor_sync(0xffffffffu, p, o));
+      m[u] = bmax_fold(p);
+    }
+    // the N divisions of a row's lanes, one a lane
+    static_assert(N == 4 && LPR >= 4, "four rows a thread");
+    const float mine = c & 2 ? (c & 1 ? m[3] : m[2]) : (c & 1 ? m[1] : m[0]);
+    const float sc1 = __fdiv_rn(mine, 127.0f), rcp1 = sc1 >= 0x1p-120f ? __frcp_rn(sc1) : 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xe = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-        const float q = xe * rcp;
-        t[e] = __fadd_rn(q, kMagic);
-        dm = fmaxf(dm, fabsf(__fsub_rn(q, __fsub_rn(t[e], kMagic))));
-      }
-      if (dm >= kBand || slow) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          t[e] = quant_exact(__uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16), sc);
-      }
-      if (dst[u] >= 0) {
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = __byte_perm(__float_as_uint(t[2 * e]), __float_as_uint(t[2 * e + 1]), 0x0040);
-        out[dst[u] * LPR + c] = make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
-        if (c == 0) scale[dst[u]] = sc;
+    for (int u = 0; u < N; ++u) {
+      const float sc = __shfl_sync(0xffffffffu, sc1, u, LPR), rcp = __shfl_sync(0xffffffffu, rcp1, u, LPR);
+      const uint2 q = quant8({x[u].x, x[u].y, x[u].z, x[u].w}, sc, rcp);
+      const long long d = dst[u % kWriteRows];
+      if (d >= 0) {
+        reinterpret_cast<uint2*>(u < kWriteRows ? kd : vd)[d * LPR + c] = q;
+        if (c == 0) const_cast<float*>(u < kWriteRows ? a.k_scale : a.v_scale)[d] = sc;
       }
     }
   }
@@ -169,9 +180,12 @@ __global__ void __launch_bounds__(kKvThreads) paged_read_kernel(const PagedArgs 
 
 cudaError_t launch_paged_write(const PagedArgs& a, bool int8, const __nv_bfloat16* k, const __nv_bfloat16* v,
                                long long k_stride, long long v_stride, cudaStream_t st) {
-  const long long rpb = kKvThreads / (a.d / 8) * kWriteRows;
-  const dim3 grid(unsigned(((long long)a.max_q * a.Hkv + rpb - 1) / rpb), 2, a.S);
-  auto go = [&](auto f) { f<<<grid, kKvThreads, 0, st>>>(a, k, v, k_stride, v_stride); };
+  const int rows = kKvThreads / (a.d / 8) * kWriteRows;   // of a CTA
+  int shift = 0;
+  while ((1 << shift) < rows && (1 << shift) < a.max_q) ++shift;
+  const int heads = rows >> shift;
+  const dim3 grid((a.max_q + (1 << shift) - 1) >> shift, (a.Hkv + heads - 1) / heads, a.S);
+  auto go = [&](auto f) { f<<<grid, kKvThreads, 0, st>>>(a, k, v, k_stride, v_stride, shift); };
   if (a.d == 128) int8 ? go(paged_write_kernel<128, true>) : go(paged_write_kernel<128, false>);
   else int8 ? go(paged_write_kernel<64, true>) : go(paged_write_kernel<64, false>);
   return cudaGetLastError();
