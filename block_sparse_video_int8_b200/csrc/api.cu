@@ -108,6 +108,19 @@ int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int ele
   return BSVA_OK;
 }
 
+int encode_map_4d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t n1, uint64_t n2, uint64_t n3,
+                  const uint64_t stride[3], uint32_t box_inner, uint32_t box1, uint32_t box2, const char* what) {
+  cuuint64_t dims[4] = {inner, n1, n2, n3};
+  cuuint64_t strides[3] = {stride[0], stride[1], stride[2]};
+  cuuint32_t box[4] = {box_inner, box1, box2, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(BSVA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, int(r));
+  return BSVA_OK;
+}
+
 }  // namespace bsva
 
 namespace {

@@ -19,6 +19,9 @@ int get_encoder();   // the driver's tensor-map encoder, looked up once; before 
 // 3-D map over [heads][rows][inner] with a box of [1][box_rows][box_inner].
 int encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t inner, uint64_t rows,
                uint64_t heads, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw, const char* what);
+// 4-D bf16 map [n3][n2][n1][inner] with byte strides of n1, n2, n3, boxes of [1][box2][box1][box_inner], 128-byte swizzle.
+int encode_map_4d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t n1, uint64_t n2, uint64_t n3,
+                  const uint64_t stride[3], uint32_t box_inner, uint32_t box1, uint32_t box2, const char* what);
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -34,13 +34,15 @@ struct PagedArgs {
   int S, T, Hkv, G, d;
   int max_q, max_kv;
   int causal, window;
+  int q_tma;                    // tile kernel: Q by TMA (G divides 128)
   int nsplit, split_keys;       // rows kernel: keys of a split; tile kernel: splits share a row tile's key tiles
   uint64_t wait_limit_ns;
 };
 
 // bf16 keys and values for the tile kernel, [heads of all pages][rows][d]; boxes of box_rows rows x 64 values.
+// Queries (q_tma) [sequences][tokens][heads][d], boxes of 128 rows x 64 values.
 struct PagedMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v, q;
 };
 
 // A sequence as the kernels use it. Values that the caller's device arrays hold are clamped into the

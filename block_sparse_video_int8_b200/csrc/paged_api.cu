@@ -123,14 +123,22 @@ int run_paged(PagedArgs& a, bool int8, const Plan& p, const PagedWs& w, void* wo
   a.part_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
   a.part_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + w.part_ml) : nullptr;
   PagedMaps maps{};
-  if (p.tiles && !int8) {
+  if (p.tiles) {
     int rc;
     a.box_rows = a.page_table && a.page_rows < 128 ? a.page_rows : 128;
     if ((rc = get_encoder())) return rc;
-    for (int z = 0; z < 2; ++z)
+    for (int z = 0; z < 2 && !int8; ++z)
       if ((rc = encode_map(z ? &maps.v : &maps.k, z ? a.v : a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.d, a.page_rows,
                            uint64_t(a.n_pages) * a.Hkv, 64, a.box_rows, CU_TENSOR_MAP_SWIZZLE_128B, z ? "v" : "k")))
         return rc;
+    a.q_tma = 128 % a.G == 0;
+    if (a.q_tma) {
+      const uint64_t tokens = a.q_start ? a.T : a.max_q, seqs = a.q_start ? 1 : a.S;
+      const uint64_t stride[3] = {uint64_t(a.q_head) * 2, uint64_t(a.q_tok) * 2,
+                                  uint64_t(a.q_start ? tokens * a.q_tok : a.q_seq) * 2};
+      if ((rc = encode_map_4d(&maps.q, a.q, a.d, uint64_t(a.Hkv) * a.G, tokens, seqs, stride, 64, a.G, 128 / a.G, "q")))
+        return rc;
+    }
   }
   cudaError_t e = p.tiles ? launch_paged_tiles(a, maps, int8, st) : launch_paged_rows(a, int8, st);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
