@@ -77,15 +77,18 @@ __device__ __forceinline__ SeqView seq_view(const PagedArgs& a, int s) {
   return r;
 }
 
-// The page that holds token t of sequence s; an entry outside [0, n_pages) is recorded and read as page 0.
+// The page table's entry for token t of sequence s, and the page that it names: one outside [0, n_pages) is recorded
+// and read as page 0.
+__device__ __forceinline__ int page_entry(const PagedArgs& a, int s, int t) {
+  return __ldg(a.page_table + size_t(s) * a.max_pages + (t >> a.page_shift));
+}
+__device__ __forceinline__ int checked_page(const PagedArgs& a, int entry) {
+  if (unsigned(entry) < unsigned(a.n_pages)) return entry;
+  atomicOr(a.status, kStatusBounds);
+  return 0;
+}
 __device__ __forceinline__ int page_of(const PagedArgs& a, int s, int t) {
-  if (!a.page_table) return s;
-  int p = __ldg(a.page_table + size_t(s) * a.max_pages + (t >> a.page_shift));
-  if (unsigned(p) >= unsigned(a.n_pages)) {
-    atomicOr(a.status, kStatusBounds);
-    p = 0;
-  }
-  return p;
+  return a.page_table ? checked_page(a, page_entry(a, s, t)) : s;
 }
 
 // Row index (of d elements, or of one scale) of token t of a head, in the page that page_of gave.

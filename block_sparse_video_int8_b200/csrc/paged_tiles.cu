@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       mbar_init(&sm.item_empty[i], 9 + kQWarps + kLoadWarps);
     }
     for (int i = 0; i < MS; ++i) mbar_init(&sm.m_full[i], 4);
-    mbar_init(&sm.r_full, 4);
+    mbar_init(&sm.r_full, kLoadWarps);
     mbar_init(&sm.v_raw, 1);
     mbar_init(&sm.next_full, 1);
     mbar_init(&sm.next_go, 1);
@@ -467,44 +467,62 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       regs_down<120>();
       // ---------------------------------------------------------------------------- key tiles, INT8 codes
       const int lt = tid - 384;
-      constexpr int CPR = D / 16, RP = 128 / CPR, NP = KT / RP;   // 16-byte chunks a row, rows a pass, passes
-      const int c = lt % CPR, r0 = lt / CPR;
+      constexpr int CPR = D / 16, RP = 128 / CPR, NP = KT / RP;   // 16-byte pieces a row, rows a pass, passes
+      // Piece c of row r0 + a pass's. For rows of 128 bytes, eight lanes take four pieces of two rows, whose widened
+      // chunks (2 c and 2 c + 1, exclusive-or the row) lie in eight different banks.
+      const int c = D == 128 ? (lt & 3) | ((lt >> 1) & 4) : lt % CPR;
+      const int r0 = D == 128 ? ((lt >> 2) & 1) | ((lt >> 4) << 1) : lt / CPR;
+      static_assert(KT == 128, "a thread looks after key lt of the tile");
+      char* const to0 = static_cast<char*>(chunk_at<D>(sm.k[0], r0, 2 * c));       // in the first stage of K
+      char* const to1 = static_cast<char*>(chunk_at<D>(sm.k[0], r0, 2 * c + 1));
+      constexpr int kStage = KT * D * 2, kPass = RP * 128;                         // RP is a multiple of 8 rows
+      const int k_to_v = int(reinterpret_cast<char*>(sm.v[0]) - reinterpret_cast<char*>(sm.k[0]));
       auto arrive = [&](uint64_t* bar) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       };
       Item it;
-      uint32_t gt = 0, turn = 0;                   // key tiles and r_full phases so far
+      uint32_t gt = 0, turn = 0;                 // key tiles and r_full phases so far
       bool ok = true;
       for (uint32_t no = 0; ok && take(it, no); ++no) {
-        // the page table is read once a key (lt of the tile), a tile ahead of the loads that need it
-        auto row_of = [&](int j) -> long long {
-          const int key = (it.t0 + j) * KT + lt;
-          return j < it.N && key >= it.lo_all && key < it.kv ? (long long)kv_row(a, page_of(a, it.s, key), it.h, key) : -1;
-        };
-        uint4 kr[NP], vr[NP];
-        auto load = [&](const void* base, uint4 (&x)[NP], uint32_t slot) {
-  #pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const long long row = sm.rows[slot & 1][p * RP + r0];
-            x[p] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(base) + row * CPR + c) : make_uint4(0, 0, 0, 0);
-          }
-        };
-        float sk = 0.f, svv = 0.f;
-        auto load_scales = [&](long long row) {
-          sk = row >= 0 ? __ldg(a.k_scale + row) : 0.f;
-          svv = row >= 0 ? __ldg(a.v_scale + row) : 0.f;
-        };
         if (it.N == 0) {
           if (lt == 0) mbar_arrive(&sm.next_go);
           __syncwarp();
           continue;
         }
-        long long next = row_of(0);
+        // The page table is read once a key, two tiles ahead of the keys, and looked at a tile later: a look at once
+        // would wait for it. -1: no key.
+        auto key_of = [&](int j) { return (it.t0 + j) * KT + lt; };
+        auto live = [&](int j) { return j < it.N && key_of(j) >= it.lo_all && key_of(j) < it.kv; };
+        auto entry = [&](int j) { return live(j) ? page_entry(a, it.s, key_of(j)) : 0; };
+        auto row_of = [&](int j, int e) -> long long {
+          return live(j) ? (long long)kv_row(a, checked_page(a, e), it.h, key_of(j)) : -1;
+        };
+        uint4 kr[NP], vr[NP];
+        auto load = [&](const void* base, uint4 (&x)[NP], uint32_t slot) {
+          const char* from = static_cast<const char*>(base) + 16 * c;
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const long long row = sm.rows[slot & 1][p * RP + r0];
+            x[p] = make_uint4(0, 0, 0, 0);
+            if (row >= 0) x[p] = __ldg(reinterpret_cast<const uint4*>(from + row * D));
+          }
+        };
+        float sk = 0.f, svv = 0.f;
+        auto load_scales = [&](long long row) {
+          sk = svv = 0.f;
+          if (row >= 0) {
+            sk = __ldg(a.k_scale + row);
+            svv = __ldg(a.v_scale + row);
+          }
+        };
+        int ahead = entry(1);
+        long long next = row_of(0, entry(0));
         sm.rows[gt & 1][lt] = next;
         load_scales(next);
-        next = row_of(1);
+        next = row_of(1, ahead);
+        ahead = entry(2);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.r_full);
         if (!(ok = wait(&sm.r_full, turn++))) break;
@@ -537,22 +555,25 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.m_full[ms]);
-  #pragma unroll
+          const int at = st * kStage;
+#pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t o[8];
             widen_bf16(__byte_perm(kr[p].x, 0, 0x3120), o[0], o[1]);
             widen_bf16(__byte_perm(kr[p].y, 0, 0x3120), o[2], o[3]);
             widen_bf16(__byte_perm(kr[p].z, 0, 0x3120), o[4], o[5]);
             widen_bf16(__byte_perm(kr[p].w, 0, 0x3120), o[6], o[7]);
-            *static_cast<uint4*>(chunk_at<D>(sm.k[st], p * RP + r0, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *static_cast<uint4*>(chunk_at<D>(sm.k[st], p * RP + r0, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(to0 + at + p * kPass) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(to1 + at + p * kPass) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           arrive(&sm.k_full[st]);
           if (j + 1 < it.N) load(a.k, kr, gt + 1);
           load_scales(next);
-          next = row_of(j + 2);
+          next = row_of(j + 2, ahead);
+          ahead = entry(j + 3);
           if (gt >= 2 && !(ok = wait(&sm.v_empty[st], (gt >> 1) - 1))) break;
-  #pragma unroll
+          if (!(ok = wait(&sm.m_full[ms], gt / MS))) break;       // sv of the other warps
+#pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t o[8];
             widen_f16(vr[p].x, o[0], o[1]);
@@ -565,8 +586,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
               const __half2 w = __hmul2(*reinterpret_cast<__half2*>(&o[e]), f);
               o[e] = *reinterpret_cast<const uint32_t*>(&w);
             }
-            *static_cast<uint4*>(chunk_at<D>(sm.v[st], p * RP + r0, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *static_cast<uint4*>(chunk_at<D>(sm.v[st], p * RP + r0, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(to0 + k_to_v + at + p * kPass) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(to1 + k_to_v + at + p * kPass) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           arrive(&sm.v_full[st]);
           if (j + 1 < it.N) load(a.v, vr, gt + 1);
