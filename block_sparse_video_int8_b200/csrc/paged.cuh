@@ -99,26 +99,10 @@ __device__ __forceinline__ size_t kv_row(const PagedArgs& a, int page, int head,
 
 // ---- widening: each 32-bit word holds four INT8 codes b0..b3; the two results hold the pairs (b0, b2)
 // and (b1, b3). Callers choose which element sits in which byte, or which order the pairs stand for.
-// bf16: 0x4300 | (b & 0x7f) = 128 + (b & 0x7f) and 0x4300 | (b & 0x80) = 128 or 256; the difference is
-// the signed code, exactly (all terms are integers of at most 8 bits).
-__device__ __forceinline__ uint32_t lop_and_or(uint32_t x, uint32_t m, uint32_t o) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(o));   // (x & m) | o
-  return r;
-}
 __device__ __forceinline__ uint32_t lop_and_xor(uint32_t x, uint32_t m, uint32_t o) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(r) : "r"(x), "r"(m), "r"(o));   // (x & m) ^ o
   return r;
-}
-__device__ __forceinline__ void widen_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
-  auto half = [](uint32_t x) {
-    uint32_t lo = lop_and_or(x, 0x007f007fu, 0x43004300u), hi = lop_and_or(x, 0x00800080u, 0x43004300u);
-    __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&lo), *reinterpret_cast<__nv_bfloat162*>(&hi));
-    return *reinterpret_cast<uint32_t*>(&d);
-  };
-  even = half(w);
-  odd = half(w >> 8);
 }
 // f16: 0x6400 | (b + 128) = 1024 + 128 + b, minus 1152.
 __device__ __forceinline__ void widen_f16(uint32_t w, uint32_t& even, uint32_t& odd) {

@@ -20,7 +20,7 @@
 //                   cp.async otherwise.
 //   warp 11         finds the next item.
 // The scales of INT8 keys enter in the softmax, x = S * (s_k scale log2 e), a vector of 128 a tile; those of the
-// values in their f16 widening, v8 * (s_v c) with the power of two c (paged.cuh), which costs a value a rounding of
+// values in their f16 widening, v8 * (s_v c) 2^-12 with the power of two c (paged.cuh), which costs a value a rounding of
 // 2^-11 at most, as the f16 weight has one. (Both scales as vectors of the softmax took 4000 cycles a half and tile
 // where one takes 2600.)
 // Widened words hold four codes as pairs (0, 2), (1, 3): K's bytes are put in order first; V's columns, and so
@@ -55,7 +55,7 @@ struct __align__(1024) TileSmem {
   float rs[MS];                         // INT8: c of this tile / c of the last one
   float cn[MS];                         // INT8: c
   uint32_t red[2][4];
-  long long rows[2][KT];                // INT8: cache row of each key of the tile whose loads come next, -1: none
+  int rows[2][KT];                      // INT8: cache row of each key of the tile whose loads come next, -1: none
   uint4 stage[8][32 * 4];               // a softmax warp's rows on their way out: 64 bytes of each of 32
   uint4 next_cta;                       // answer to the request for a waiting CTA
   Item item[2];
@@ -110,6 +110,33 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// Widening with one multiply-add a pair: a code b xor 0x80 = b + 128 in the low byte of a 16-bit float is the subnormal
+// (b + 128) 2^-133 (bf16) or 2^-24 (f16), which both the multiply-add and its exact product take as it is. Words hold
+// four codes b0 .. b3, the results the pairs (b0, b2) and (b1, b3).
+// bf16: (b + 128) 2^-133 * 2^127 - 2 = b / 64, exact.
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
+  auto pair = [](uint32_t x) {
+    uint32_t u = lop_and_xor(x, 0x00ff00ffu, 0x00800080u), r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(0x7f007f00u), "r"(0xc000c000u));
+    return r;
+  };
+  even = pair(w);
+  odd = pair(w >> 8);
+}
+// f16 times f (a pair of equal f16): (b + 128) 2^-24 * f - 2^-17 f = b (2^-24 f), rounded once; 2^-17 f is exact, or
+// off by at most 2^-25 where it is subnormal, as the result then is.
+__device__ __forceinline__ void values_f16(uint32_t w, uint32_t f, uint32_t& even, uint32_t& odd) {
+  uint32_t c;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(f), "r"(0x80808080u));   // two of -2^-17
+  auto pair = [&](uint32_t x) {
+    uint32_t u = lop_and_xor(x, 0x00ff00ffu, 0x00800080u), r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(f), "r"(c));
+    return r;
+  };
+  even = pair(w);
+  odd = pair(w >> 8);
 }
 
 template <int N>
@@ -183,9 +210,19 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
   auto wait = [&](uint64_t* bar, uint32_t par) {
     return __all_sync(0xffffffffu, mbar_wait(bar, par & 1, abort, a.status, lim)) != 0;
   };
+  // the same for warps that wait for most of the time: their polls would take issue slots from the others
+  auto wait_idle = [&](uint64_t* bar, uint32_t par) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!__all_sync(0xffffffffu, mbar_test_wait(bar, par & 1))) {
+      __nanosleep(200);
+      if (__any_sync(0xffffffffu, *abort != 0 || globaltimer_ns() - t0 > lim))
+        return wait(bar, par);                   // which gives up the usual way
+    }
+    return true;
+  };
   // item `no` for this warp: false when there are no more (or a wait ran out)
-  auto take = [&](Item& it, uint32_t no) -> bool {
-    if (!wait(&sm.item_full[no & 1], no >> 1)) return false;
+  auto take = [&](Item& it, uint32_t no, bool idle = false) -> bool {
+    if (!(idle ? wait_idle(&sm.item_full[no & 1], no >> 1) : wait(&sm.item_full[no & 1], no >> 1))) return false;
     it = sm.item[no & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[no & 1]);
@@ -395,7 +432,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         if (!(alive = wait(&sm.pv_done[hf][1], cnt - 1))) break;
         tc_fence_after();
       }
-      const float up = I8 && cn != 0.f ? 1.f / cn : 1.f;
+      const float up = I8 && cn != 0.f ? 4096.f / cn : 1.f;
       const float inv = a.nsplit > 1 ? up : l > 0.f ? up / l : 0.f;
       const size_t pr = size_t(it.sp) * a.out_rows + (off < 0 ? 0 : off / D);
       if (it.N > 0 || a.nsplit == 1) {           // a split without keys leaves its output part unwritten
@@ -496,21 +533,21 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         auto key_of = [&](int j) { return (it.t0 + j) * KT + lt; };
         auto live = [&](int j) { return j < it.N && key_of(j) >= it.lo_all && key_of(j) < it.kv; };
         auto entry = [&](int j) { return live(j) ? page_entry(a, it.s, key_of(j)) : 0; };
-        auto row_of = [&](int j, int e) -> long long {
-          return live(j) ? (long long)kv_row(a, checked_page(a, e), it.h, key_of(j)) : -1;
+        auto row_of = [&](int j, int e) -> int {   // fits: 2^31 rows would be 275 GB of codes
+          return live(j) ? int(kv_row(a, checked_page(a, e), it.h, key_of(j))) : -1;
         };
         uint4 kr[NP], vr[NP];
         auto load = [&](const void* base, uint4 (&x)[NP], uint32_t slot) {
           const char* from = static_cast<const char*>(base) + 16 * c;
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const long long row = sm.rows[slot & 1][p * RP + r0];
+            const int row = sm.rows[slot & 1][p * RP + r0];
             x[p] = make_uint4(0, 0, 0, 0);
-            if (row >= 0) x[p] = __ldg(reinterpret_cast<const uint4*>(from + row * D));
+            if (row >= 0) x[p] = __ldg(reinterpret_cast<const uint4*>(from + (long long)row * D));
           }
         };
         float sk = 0.f, svv = 0.f;
-        auto load_scales = [&](long long row) {
+        auto load_scales = [&](int row) {
           sk = svv = 0.f;
           if (row >= 0) {
             sk = __ldg(a.k_scale + row);
@@ -518,7 +555,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           }
         };
         int ahead = entry(1);
-        long long next = row_of(0, entry(0));
+        int next = row_of(0, entry(0));
         sm.rows[gt & 1][lt] = next;
         load_scales(next);
         next = row_of(1, ahead);
@@ -547,8 +584,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
             if (cn != 0.f) rs = n / cn;
             cn = n;
           }
-          sm.fk[ms][lt] = sk * a.scale_log2;
-          sm.sv[st][lt] = pack_f16x2(svv * cn, svv * cn);
+          sm.fk[ms][lt] = sk * (64.f * a.scale_log2);                           // K enters as code / 64
+          sm.sv[st][lt] = pack_f16x2(svv * cn * 4096.f, svv * cn * 4096.f);     // times 2^-24: V as code * s_v c / 4096
           if (lt == 0) {
             sm.rs[ms] = rs;
             sm.cn[ms] = cn;
@@ -559,10 +596,10 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t o[8];
-            widen_bf16(__byte_perm(kr[p].x, 0, 0x3120), o[0], o[1]);
-            widen_bf16(__byte_perm(kr[p].y, 0, 0x3120), o[2], o[3]);
-            widen_bf16(__byte_perm(kr[p].z, 0, 0x3120), o[4], o[5]);
-            widen_bf16(__byte_perm(kr[p].w, 0, 0x3120), o[6], o[7]);
+            codes_bf16(__byte_perm(kr[p].x, 0, 0x3120), o[0], o[1]);
+            codes_bf16(__byte_perm(kr[p].y, 0, 0x3120), o[2], o[3]);
+            codes_bf16(__byte_perm(kr[p].z, 0, 0x3120), o[4], o[5]);
+            codes_bf16(__byte_perm(kr[p].w, 0, 0x3120), o[6], o[7]);
             *reinterpret_cast<uint4*>(to0 + at + p * kPass) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(to1 + at + p * kPass) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -576,16 +613,11 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             uint32_t o[8];
-            widen_f16(vr[p].x, o[0], o[1]);
-            widen_f16(vr[p].y, o[2], o[3]);
-            widen_f16(vr[p].z, o[4], o[5]);
-            widen_f16(vr[p].w, o[6], o[7]);
-            const __half2 f = *reinterpret_cast<const __half2*>(&sm.sv[st][p * RP + r0]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 w = __hmul2(*reinterpret_cast<__half2*>(&o[e]), f);
-              o[e] = *reinterpret_cast<const uint32_t*>(&w);
-            }
+            const uint32_t f = sm.sv[st][p * RP + r0];
+            values_f16(vr[p].x, f, o[0], o[1]);
+            values_f16(vr[p].y, f, o[2], o[3]);
+            values_f16(vr[p].z, f, o[4], o[5]);
+            values_f16(vr[p].w, f, o[6], o[7]);
             *reinterpret_cast<uint4*>(to0 + k_to_v + at + p * kPass) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(to1 + k_to_v + at + p * kPass) = make_uint4(o[4], o[5], o[6], o[7]);
           }
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           }
         }
         if (it.nh > 0 || !more) {
-          if (no >= 2 && !wait(&sm.item_empty[no & 1], (no >> 1) - 1)) break;
+          if (no >= 2 && !wait_idle(&sm.item_empty[no & 1], (no >> 1) - 1)) break;
           if (lane == 0) {
             sm.item[no & 1] = it;
             mbar_arrive(&sm.item_full[no & 1]);
@@ -636,7 +668,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           if (!more) break;
           // the next one is asked for when this one's last key tile is: no sooner, so that none waits here while
           // another SM is idle
-          if (!wait(&sm.next_go, no)) break;
+          if (!wait_idle(&sm.next_go, no)) break;
           ++no;
         }
         if (lane == 0) {
@@ -656,12 +688,12 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       Item it;
       uint32_t used[2] = {0, 0};
       bool ok = true;
-      for (uint32_t no = 0; ok && take(it, no); ++no) {
+      for (uint32_t no = 0; ok && take(it, no, true); ++no) {
         if (it.N == 0) continue;
   #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           if (hf >= it.nh || !ok) break;
-          if (used[hf] > 0 && !(ok = wait(&sm.q_empty[hf], used[hf] - 1))) break;
+          if (used[hf] > 0 && !(ok = wait_idle(&sm.q_empty[hf], used[hf] - 1))) break;
           ++used[hf];
           if (a.q_tma) {                         // a box of G heads and 128 / G tokens a panel, by the first of the warps
             if (lane == 0) {
