@@ -73,7 +73,7 @@ Plan make_plan(int S, int Hkv, int G, int max_q, int keys, int d, bool int8) {
     // from measured rates: 128 keys take an item 3.2 us with INT8 codes, 1.95 us with bf16 (head dim 64: 0.6 of it),
     // partial outputs move at 5.5 TB/s, the second kernel costs 4 us. (2048 x 32760 tokens, 320 items: n = 1 2486 us.)
     const long long items = (rows + 255) / 256 * Hkv * S, tiles = (keys + 127) / 128;
-    const long long most = tiles / 4, room = 148 * 9 / items;   // splits of four key tiles at least
+    const long long most = tiles / 2, room = 148 * 9 / items;   // splits of two key tiles at least
     long long cap = most < room ? most : room;
     cap = cap < kMaxSplits ? cap : kMaxSplits;
     p.cap = int(cap < 1 ? 1 : cap);

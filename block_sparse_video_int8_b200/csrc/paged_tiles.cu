@@ -104,14 +104,6 @@ __device__ __forceinline__ bool next_cta(const uint4* answer, int& x, int& y, in
   return got != 0;
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
 // Widening with one multiply-add a pair: a code b xor 0x80 = b + 128 in the low byte of a 16-bit float is the subnormal
 // (b + 128) 2^-133 (bf16) or 2^-24 (f16), which both the multiply-add and its exact product take as it is. Words hold
 // four codes b0 .. b3, the results the pairs (b0, b2) and (b1, b3).
@@ -377,49 +369,64 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           ahead = done;
           if (late) publish(0);
           if ((I8 || looked) && __any_sync(0xffffffffu, f != 1.f) && !(alive = rescale(sub))) break;
-          if (done) {
-            tmem_st32(tS + col, pk);
-          } else {
-            // Logits are rounded before the maximum is taken off (fused, those past 2^24 would come out above it by
-            // half their own step), so the largest is exactly 0.
-            float mx = -INFINITY;
-            uint32_t w[16];
+          if (!done) {
+            // scaled logits of 32 columns in xa, -inf where the row does not see. They are rounded before the maximum is
+            // taken off (fused, those past 2^24 would come out above it by half their own step), so the largest is
+            // exactly 0.
+            auto masked = [&](int c0) {
+              tmem_ld32(tS + col + c0, xa);
+              tmem_wait_ld(xa);
+              const int l0 = clo - col - c0, h0 = chi - col - c0;
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                float4 f4 = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
+                if constexpr (I8) f4 = *reinterpret_cast<const float4*>(fkp + col + c0 + c);
+                const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float y = __fmul_rn(__uint_as_float(xa[c + e]), fs[e]);
+                  if (c + e < l0 || c + e > h0) y = -INFINITY;
+                  xa[c + e] = __float_as_uint(y);
+                }
+              }
+            };
+            looked = __any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll 1
-            for (int step = 0; step < 4; ++step) {   // the maximum of 2 x 32 columns, then their weights
-              const int c0 = col + 32 * (step & 1), l0 = clo - c0, h0 = chi - c0;
-              if (step == 2) {
+            while (true) {
+              if (looked) {
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c0 = 0; c0 < 64; c0 += 32) {
+                  masked(c0);
+                  float top = -INFINITY;
+#pragma unroll
+                  for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(xa[c]), __uint_as_float(xa[c + 1])));
+                  mx = fmaxf(mx, top);
+                }
                 raise(mx);
                 if (__any_sync(0xffffffffu, f != 1.f) && !(alive = rescale(sub))) break;
               }
               const float mu = m == -INFINITY ? 0.f : m;
-              tmem_ld32(tS + c0, xa);
-              tmem_wait_ld(xa);
-              float top = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                float y = __fmul_rn(__uint_as_float(xa[c]), I8 ? fkp[c0 + c] : a.scale_log2);
-                if (c < l0 || c > h0) y = -INFINITY;
-                xa[c] = __float_as_uint(y);
-              }
-              if (step < 2) {
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(__uint_as_float(xa[c]), __uint_as_float(xa[c + 1])));
-                mx = fmaxf(mx, top);
-              } else {
-                float2 acc = make_float2(0.f, 0.f);
+              float2 acc = make_float2(0.f, 0.f);
+              auto weigh = [&](int c0) {
+                masked(c0);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                   const float2 p = make_float2(ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c]), -mu)),
                                                ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c + 1]), -mu)));
                   acc = __fadd2_rn(acc, p);
-                  w[c] = I8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
+                  pk[c0 / 2 + c] = I8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
                 }
-                ls = (step == 2 ? 0.f : ls) + (acc.x + acc.y);
-                tmem_st16(tS + col + 16 * (step & 1), w);
-              }
+              };
+              weigh(0);
+              weigh(32);
+              ls = acc.x + acc.y;
+              if (looked || __all_sync(0xffffffffu, ls <= kFar)) break;
+              looked = true;
             }
             if (!alive) break;
           }
+          tmem_st32(tS + col, pk);
           l += ls;
         }
         if (!alive) break;
