@@ -23,7 +23,8 @@ struct PagedArgs {
   __nv_bfloat16* out;
   float* lse;                   // [out rows], nullable
   float* part_o;                // [nsplit, out rows, d] unnormalised partial outputs
-  float2* part_ml;              // [nsplit, out rows] (running max in log2 units, sum)
+  float4* part_ml;              // [nsplit, out rows] (running max in log2 units, sum that divides O, sum of the
+                                // unrounded weights, unused)
   uint32_t* status;
   long long q_seq, q_tok, q_head;   // q strides (q_seq: contiguous source only)
   long long o_seq, o_tok, o_head;   // out strides; out row index = offset / d

@@ -66,7 +66,10 @@ struct Plan {
 Plan make_plan(int S, int Hkv, int G, int max_q, int keys, int d, bool int8) {
   Plan p;
   const long long rows = (long long)max_q * G;
-  p.tiles = rows > 16;
+  // Tiles of 256 rows pay from some rows on; below, row tiles of 16 that read the keys again are faster. 8 sequences of
+  // 8192 keys, 8 key heads, tiles / rows, us: INT8 24 rows 113 / 65, 48 rows 117 / 80, 100 rows 123 / 115 (one sequence
+  // of 30000 keys 72 / 117), 200 rows 142 / 197; bf16 24 rows 73 / 68, 48 rows 74 / 80, 100 rows 75 / 117.
+  p.tiles = rows > (int8 ? 64 : 32);
   if (p.tiles) {
     // An item is 256 rows over all keys, one at a time an SM. Splitting the keys n ways levels the last round (and
     // fills the SMs where there are few items), and costs writing and joining n partial outputs. The time of each n
@@ -81,7 +84,7 @@ Plan make_plan(int S, int Hkv, int G, int max_q, int keys, int d, bool int8) {
     double best = 0;
     for (int n = 1; n <= p.cap; ++n) {
       const double t = double((items * n + 147) / 148) * double((tiles + n - 1) / n) * step +
-                       (n > 1 ? 4.0 + double(n) * rows * Hkv * S * (8.0 * d + 16.0) / 5.5e6 : 0.0);
+                       (n > 1 ? 4.0 + double(n) * rows * Hkv * S * (8.0 * d + 32.0) / 5.5e6 : 0.0);
       if (n == 1 || t < best) {
         best = t;
         p.nsplit = n;
@@ -110,13 +113,13 @@ Plan make_plan(int S, int Hkv, int G, int max_q, int keys, int d, bool int8) {
 
 size_t align256z(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Status word, then the partial outputs and their (max, sum) pairs.
+// Status word, then the partial outputs and their maxima and sums.
 struct PagedWs {
   size_t part_o = 256, part_ml = 0, total = 256;
   PagedWs(int cap, size_t out_rows, int d) {
     if (cap < 2) return;
     part_ml = align256z(part_o + size_t(cap) * out_rows * d * 4);
-    total = align256z(part_ml + size_t(cap) * out_rows * 8);
+    total = align256z(part_ml + size_t(cap) * out_rows * 16);
   }
 };
 
@@ -134,7 +137,7 @@ int run_paged(PagedArgs& a, bool int8, const Plan& p, const PagedWs& w, void* wo
   a.nsplit = p.nsplit;
   a.split_keys = p.split_keys;
   a.part_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
-  a.part_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + w.part_ml) : nullptr;
+  a.part_ml = p.nsplit > 1 ? reinterpret_cast<float4*>(ws + w.part_ml) : nullptr;
   PagedMaps maps{};
   if (p.tiles) {
     int rc;

@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       c1 = vs[1] * cn;
     }
     // ---- weights, transposed into the B operand of the second product
-    uint32_t bp[NT][2];
+    // (bf16 values: the weights enter as two bf16 terms, since one would add as much error as the output's rounding)
+    uint32_t bp[NT][2], bl[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float p[4];
@@ -336,8 +337,18 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
         p[e] = ex2_approx(x[nt][e] - mu);
         l[nt][e & 1] += p[e];
       }
-      bp[nt][0] = transpose_8x8(I8 ? pack_f16x2(p[0] * c0, p[1] * c0) : pack_bf16x2(p[0], p[1]));
-      bp[nt][1] = transpose_8x8(I8 ? pack_f16x2(p[2] * c1, p[3] * c1) : pack_bf16x2(p[2], p[3]));
+      if constexpr (I8) {
+        bp[nt][0] = transpose_8x8(pack_f16x2(p[0] * c0, p[1] * c0));
+        bp[nt][1] = transpose_8x8(pack_f16x2(p[2] * c1, p[3] * c1));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+          bp[nt][e] = transpose_8x8(w);
+          bl[nt][e] = transpose_8x8(pack_bf16x2(p[2 * e] - __uint_as_float(w << 16),
+                                                p[2 * e + 1] - __uint_as_float(w & 0xffff0000u)));
+        }
+      }
     }
     // ---- O^T: word w of the lane's V pieces gives d values in pairs, tile rows (2t, 2t+1) and (2t+8, 2t+9)
     uint32_t vr[4][VW];
@@ -372,7 +383,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
         for (int nt = 0; nt < NT; ++nt) mma_16x8x16<true>(o[nt][2 * w + 1], a0, a1, a2, a3, bp[nt][0], bp[nt][1]);
       } else {                            // d values 2w, 2w+1: one tile
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16x8x16<false>(o[nt][w], a_lo, a_hi, b_lo, b_hi, bp[nt][0], bp[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16x8x16<false>(o[nt][w], a_lo, a_hi, b_lo, b_hi, bp[nt][0], bp[nt][1]);
+          mma_16x8x16<false>(o[nt][w], a_lo, a_hi, b_lo, b_hi, bl[nt][0], bl[nt][1]);
+        }
       }
     }
   }
@@ -427,7 +441,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     if (a.nsplit > 1) {
       const size_t pr = size_t(sp) * a.out_rows + off / D;
       *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c) = y;
-      if (c == 0) a.part_ml[pr] = make_float2(mx, ls);
+      if (c == 0) a.part_ml[pr] = make_float4(mx, ls, ls, 0.f);
     } else {
       const float inv = ls > 0.f ? 1.f / ls : 0.f;
       *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
@@ -452,21 +466,22 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
   const size_t row = off / D;
   float mx = -INFINITY;
   for (int p = 0; p < a.nsplit; ++p) mx = fmaxf(mx, a.part_ml[size_t(p) * a.out_rows + row].x);
-  float ls = 0.f;
+  float ls = 0.f, le = 0.f;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p = 0; p < a.nsplit; ++p) {
     const size_t pr = size_t(p) * a.out_rows + row;
-    const float2 ml = a.part_ml[pr];
+    const float4 ml = a.part_ml[pr];
     if (ml.x == -INFINITY) continue;   // a split without a key of this row: its output part is not written
     const float f = ex2_approx(ml.x - mx);
     const float4 z = *reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c);
     ls += f * ml.y;
+    le += f * ml.z;
     y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
   }
   const float inv = ls > 0.f ? 1.f / ls : 0.f;
   *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
       make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-  if (c == 0 && a.lse) a.lse[row] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+  if (c == 0 && a.lse) a.lse[row] = le > 0.f ? (mx + log2f(le)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace

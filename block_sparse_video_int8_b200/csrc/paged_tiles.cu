@@ -25,6 +25,9 @@
 // where one takes 2600.)
 // Widened words hold four codes as pairs (0, 2), (1, 3): K's bytes are put in order first; V's columns, and so
 // O's, keep that order and the output undoes it.
+// bf16 values take bf16 weights; O is divided by the sum of the rounded ones, so that the rounding of a key that
+// outweighs the others cancels, and the log-sum-exp takes the sum of the unrounded ones (LSE). f16 weights round eight
+// times finer and need neither.
 // Every wait is bounded as in attn_sm100.cu.
 #include "paged.cuh"
 
@@ -131,6 +134,14 @@ __device__ __forceinline__ void values_f16(uint32_t w, uint32_t f, uint32_t& eve
   odd = pair(w >> 8);
 }
 
+// sum += both halves of a pair of bf16
+__device__ __forceinline__ void add_bf16x2(float& sum, uint32_t w) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\t"
+      "add.rn.f32.bf16 %0, a, %0;\n\tadd.rn.f32.bf16 %0, b, %0;\n\t}"
+      : "+f"(sum)
+      : "r"(w));
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -155,7 +166,7 @@ __device__ __forceinline__ void* chunk_at(void* tile, int row, int c) {
   return static_cast<char*>(tile) + (c / 8) * (128 * 128) + row * 128 + (((c % 8) ^ (row & 7)) * 16);
 }
 
-template <int D, bool I8>
+template <int D, bool I8, bool LSE>
 __global__ void __launch_bounds__(kTileThreads<I8>, 1)
     paged_tiles_kernel(const PagedArgs a, const __grid_constant__ PagedMaps maps) {
   extern __shared__ unsigned char smem_raw[];
@@ -221,10 +232,10 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
     return it.nh > 0;
   };
 
-  // Registers go to the softmax: INT8, 512 threads with 128 each: 2 x 168 + 56 + 120 = 4 x 128 a lane of the four
-  // warpgroups.
+  // Registers go to the softmax. INT8, 512 threads with 128 each: 2 x 168 + 56 + 120 = 4 x 128 for the four warpgroups;
+  // bf16, 384 threads with 168 each: 2 x 184 + 136 = 2 x 192 + 120 = 3 x 168, with which nothing is spilled.
   if (warp < 8) {
-    if constexpr (I8) regs_up<168>();
+    regs_up<I8 ? 168 : LSE ? 192 : 184>();
     // --------------------------------------------------------------------------------------- softmax
     const int hf = warp / 4, r = tid & 127;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         if (a.causal) hi = min(hi, pos);
         if (a.window) lo = max(0, pos - a.window + 1);
       }
-      float m = -INFINITY, l = 0.f, cn = 1.f;
+      float m = -INFINITY, l = 0.f, le = 0.f, cn = 1.f;   // l divides O, le is of the unrounded weights
       for (int j = 0; j < it.N; ++j) {
         const int ms = (gt + j) % MS;
         alive = wait(&sm.s_full[hf], cnt);
@@ -294,13 +305,14 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
 #pragma unroll 1
         for (int sub = 0; sub < 2; ++sub) {
           const int col = 64 * sub;
-          float ls = 0.f;
+          float ls = 0.f, es = 0.f;
           bool quick = whole, done = false, late = sub > 0;   // late: the first half's weights are still to be published
           auto raise = [&](float mx) {
             if (mx > m + 8.f) {
               const float al = m == -INFINITY ? 0.f : ex2_approx(m - mx);
               f *= al;
               l *= al;
+              if constexpr (LSE) le *= al;
               m = mx;
             }
           };
@@ -331,6 +343,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           while (quick) {
             const float2 nm = make_float2(-m, -m), sc = make_float2(a.scale_log2, a.scale_log2);
             float2 acc = make_float2(0.f, 0.f);
+            float ls1 = 0.f;
+            ls = 0.f;
             auto quick32 = [&](const uint32_t (&x)[32], int c0) {   // c0 = 0 or 32
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {
@@ -344,19 +358,27 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
                 const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * c + 2]), __uint_as_float(x[2 * c + 3])), f1, nm);
                 const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                 const float2 q = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-                acc = __fadd2_rn(acc, __fadd2_rn(p, q));
                 pk[c0 / 2 + c] = I8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
                 pk[c0 / 2 + c + 1] = I8 ? pack_f16x2(q.x, q.y) : pack_bf16x2(q.x, q.y);
+                if constexpr (!I8) {
+                  add_bf16x2(ls, pk[c0 / 2 + c]);
+                  add_bf16x2(ls1, pk[c0 / 2 + c + 1]);
+                }
+                if constexpr (I8 || LSE) acc = __fadd2_rn(acc, __fadd2_rn(p, q));
               }
             };
             tmem_ld32(tS + col + 32, xb);
+            // INT8 has no registers to spare, and one that a load still fills must not be spilled: it waits at once
+            if constexpr (I8) tmem_wait_ld(xb);
             quick32(xa, 0);
             if (late) publish(0);                // its stores landed under this work
             late = false;
             tmem_wait_ld(xb);
             tmem_ld32(tS + 64, xa);              // the second sub-tile's (in the second, of no use)
+            if constexpr (I8) tmem_wait_ld(xa);
             quick32(xb, 32);
-            ls = acc.x + acc.y;
+            es = acc.x + acc.y;
+            ls = I8 ? es : ls + ls1;
             tmem_wait_ld(xa);
             done = looked || __all_sync(0xffffffffu, ls <= kFar);
             if (done) break;
@@ -408,6 +430,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
               }
               const float mu = m == -INFINITY ? 0.f : m;
               float2 acc = make_float2(0.f, 0.f);
+              ls = 0.f;
               auto weigh = [&](int c0) {
                 masked(c0);
 #pragma unroll
@@ -416,11 +439,13 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
                                                ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c + 1]), -mu)));
                   acc = __fadd2_rn(acc, p);
                   pk[c0 / 2 + c] = I8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
+                  if constexpr (!I8) add_bf16x2(ls, pk[c0 / 2 + c]);
                 }
               };
               weigh(0);
               weigh(32);
-              ls = acc.x + acc.y;
+              es = acc.x + acc.y;
+              if constexpr (I8) ls = es;
               if (looked || __all_sync(0xffffffffu, ls <= kFar)) break;
               looked = true;
             }
@@ -428,6 +453,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           }
           tmem_st32(tS + col, pk);
           l += ls;
+          if constexpr (LSE) le += es;
         }
         if (!alive) break;
         publish(1);
@@ -500,8 +526,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         }
       }
       if (off >= 0) {
-        if (a.nsplit > 1) a.part_ml[pr] = make_float2(m, l);
-        else if (a.lse) a.lse[off / D] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.nsplit > 1) a.part_ml[pr] = make_float4(m, l, LSE ? le : l, 0.f);
+        else if (a.lse) a.lse[off / D] = l > 0.f ? (m + log2f(LSE ? le : l)) * 0.69314718055994531f : -INFINITY;
       }
       // the next item's first product writes O: order it after these reads (it waits for this half's weights)
       tc_fence_before();
@@ -634,7 +660,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       }
     }
   } else {
-    if constexpr (I8) regs_down<56>();
+    regs_down<I8 ? 56 : LSE ? 120 : 136>();
     if (warp == 11) {
       // ------------------------------------------------------------------------------------- next item
       int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
@@ -868,23 +894,26 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
   }
 }
 
-template <int D, bool I8>
+template <int D, bool I8, bool LSE>
 cudaError_t launch_tiles(const PagedArgs& a, const PagedMaps& maps, cudaStream_t st) {
   // one CTA an SM: its TMEM allocation is the whole of it
   const size_t need = sizeof(TileSmem<D, I8>) + 1024, smem = need > 120 * 1024 ? need : 120 * 1024;
-  cudaError_t e = cudaFuncSetAttribute(paged_tiles_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  cudaError_t e =
+      cudaFuncSetAttribute(paged_tiles_kernel<D, I8, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.max_q * a.G;
   const dim3 grid(unsigned((rows + 255) / 256 * a.nsplit), a.Hkv, a.S);
-  paged_tiles_kernel<D, I8><<<grid, kTileThreads<I8>, smem, st>>>(a, maps);
+  paged_tiles_kernel<D, I8, LSE><<<grid, kTileThreads<I8>, smem, st>>>(a, maps);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tiles(const PagedArgs& a, const PagedMaps& maps, bool int8, cudaStream_t st) {
-  if (a.d == 128) return int8 ? launch_tiles<128, true>(a, maps, st) : launch_tiles<128, false>(a, maps, st);
-  return int8 ? launch_tiles<64, true>(a, maps, st) : launch_tiles<64, false>(a, maps, st);
+  // INT8 sums the unrounded weights in any case
+  if (int8) return a.d == 128 ? launch_tiles<128, true, false>(a, maps, st) : launch_tiles<64, true, false>(a, maps, st);
+  if (a.lse) return a.d == 128 ? launch_tiles<128, false, true>(a, maps, st) : launch_tiles<64, false, true>(a, maps, st);
+  return a.d == 128 ? launch_tiles<128, false, false>(a, maps, st) : launch_tiles<64, false, false>(a, maps, st);
 }
 
 }  // namespace bsva
