@@ -122,10 +122,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// ---- INT8 values in an f16 product: a weight enters as w = p * s_v * c with c a power of two, so that w
-// fits f16 whatever the scales' range (c = 1 / 2^floor(log2 s), s the largest scale seen when c was set:
-// p <= 2^12 by the lazy running max, s_v * c < 2^3 by kScaleGrow, so w < 2^15). f16 keeps 11 bits of a
-// weight where bf16 would keep 8; the sum of the weights takes p itself, in fp32.
+// ---- INT8 values in an f16 product: the scale s_v of a key's values enters as s_v * c with c a power of two, so
+// that it fits f16 whatever the scales' range: c = 1 / 2^floor(log2 s), s the largest scale seen when c was set, and
+// s_v * c < 2^3 by kScaleGrow. Few rows: the weight is p * s_v * c < 2^11, p <= 2^8 by the lazy running maximum.
+// Tiles: the value is code * s_v * c / 4096 < 2^-2. f16 keeps 11 bits of either where bf16 would keep 8; the sum of
+// the weights takes p itself, in fp32. Scales far below the largest one reach f16's subnormals: a key's weighted
+// values are off by 2^-20 of the largest value at most.
 constexpr float kScaleGrow = 8.f;    // s_v * c reaches this: c is set anew and the output so far rescaled
 __device__ __forceinline__ float scale_norm(float s) {   // 2^-floor(log2 s), both in the normal range
   const int e = min(max(int(__float_as_uint(s) >> 23), 1), 253);

@@ -26,6 +26,9 @@ int check_cache(const bsva_paged_kv* c) {
     return fail(BSVA_ERR_INVALID_ARG, "page_size = %d; supported: 16, 32, 64, 128, 256", c->page_size);
   if (c->dtype != BSVA_KV_INT8 && c->dtype != BSVA_KV_BF16)
     return fail(BSVA_ERR_INVALID_ARG, "cache dtype = %d; use BSVA_KV_INT8 (0) or BSVA_KV_BF16 (1)", c->dtype);
+  if ((long long)c->n_pages * c->H >= (1ll << 31) / c->page_size)   // the kernels keep a row's number in an int
+    return fail(BSVA_ERR_INVALID_ARG, "cache: n_pages * H * page_size = %d * %d * %d is not below 2^31", c->n_pages, c->H,
+                c->page_size);
   return BSVA_OK;
 }
 
@@ -253,9 +256,9 @@ int paged_attn_fwd(const bsva_paged_kv* c, const bsva_paged_batch* b, const void
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(float(c->d));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.causal = causal;
-  a.window = window;
+  a.window = window >= b->max_kv ? 0 : window;   // one that hides no key is none
   // keys a sequence's rows can see: with a window, its width and the chunk's length (from a multiple of 16)
-  const long long reach = window ? (long long)window + b->max_q + 15 : b->max_kv;
+  const long long reach = a.window ? (long long)a.window + b->max_q + 15 : b->max_kv;
   const Plan p = make_plan(b->S, c->H, a.G, b->max_q, reach < b->max_kv ? int(reach) : b->max_kv, c->d, c->dtype == BSVA_KV_INT8);
   return run_paged(a, c->dtype == BSVA_KV_INT8, p, w, workspace,
                    reinterpret_cast<cudaStream_t>(stream));

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     find(key + NS * STEP);
     const unsigned char* stage = ring + st * STAGE;
     uint4 kr[2][KL];
-    float ks[2], vs[2];
+    float ks[2] = {a.scale_log2, a.scale_log2}, vs[2];   // factors of a key's logits, INT8: scales of its values
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -266,12 +266,11 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma_16x8x16<I8>(x[nt], a0, a1, a2, a3, bq[nt][kk][0], bq[nt][kk][1]);
     }
-    const float f0 = I8 ? ks[0] : a.scale_log2, f1 = I8 ? ks[1] : a.scale_log2;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // rounded here, not fused with the subtraction of the maximum, which was taken from rounded logits
-      x[nt][0] = __fmul_rn(x[nt][0] * qf[nt][0], f0); x[nt][1] = __fmul_rn(x[nt][1] * qf[nt][1], f0);
-      x[nt][2] = __fmul_rn(x[nt][2] * qf[nt][0], f1); x[nt][3] = __fmul_rn(x[nt][3] * qf[nt][1], f1);
+      x[nt][0] = __fmul_rn(x[nt][0] * qf[nt][0], ks[0]); x[nt][1] = __fmul_rn(x[nt][1] * qf[nt][1], ks[0]);
+      x[nt][2] = __fmul_rn(x[nt][2] * qf[nt][0], ks[1]); x[nt][3] = __fmul_rn(x[nt][3] * qf[nt][1], ks[1]);
     }
     if (key < full_lo || key + 16 > min(full_hi, hi)) {
 #pragma unroll

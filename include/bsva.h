@@ -384,7 +384,8 @@ int masked_block_attn_fwd_kvcache(const bsva_kv_cache* c, int Lq, const int8_t* 
  * heads: Hq is a multiple of H, query head h reads key head h / (Hq / H).
  * BSVA_KV_INT8 holds codes with one scale per (token, head): s = fl32(amax/127) over
  * the d values, code = rint_half_even(fl32(x/s)), 0 where s = 0; the cached value is
- * code * s. BSVA_KV_BF16 holds the values themselves. Values must be finite.
+ * code * s. BSVA_KV_BF16 holds the values themselves. Values must be finite: a key that
+ * holds an infinity or a NaN can spoil rows of its sequence that do not see it.
  * The caller allocates the buffers (not necessarily initialised: a row is read only
  * once it has been written). */
 enum bsva_kv_dtype {
@@ -423,8 +424,8 @@ typedef struct bsva_paged_batch {
   const int32_t* page_table;  /* device int32 [S, max_pages]                            */
 } bsva_paged_batch;
 
-/* Workspace bytes of any of the paged calls for this cache and batch and up to Hq query
- * heads; 0 on a bad geometry. Write and read need its first 256 bytes (the status word)
+/* Workspace bytes of any of the paged calls for this cache and batch (at most its T rows)
+ * and Hq query heads; 0 on a bad geometry. Write and read need its first 256 bytes (the status word)
  * only. Calls that may run at the same time need a workspace each. */
 size_t bsva_paged_workspace_bytes(const bsva_paged_kv* c, const bsva_paged_batch* b, int Hq);
 

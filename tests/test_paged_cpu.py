@@ -79,7 +79,8 @@ def test_oracle_attention_against_sdpa(n, kv, causal, window):
 @pytest.mark.parametrize("bad,code,word", [
     (dict(d=96), 2, "head dim"), (dict(page_size=24), 1, "page_size"), (dict(page_size=8), 1, "page_size"),
     (dict(page_size=512), 1, "page_size"), (dict(n_pages=0), 1, "n_pages"), (dict(H=0), 1, "H ="),
-    (dict(dtype=2), 1, "dtype"), (dict(k=None), 1, "NULL"), (dict(v=0x10008), 1, "aligned"),
+    (dict(dtype=2), 1, "dtype"), (dict(n_pages=2 ** 30, H=1, page_size=16), 1, "below 2^31"),
+    (dict(n_pages=2 ** 24, H=8, page_size=16), 1, "below 2^31"), (dict(k=None), 1, "NULL"), (dict(v=0x10008), 1, "aligned"),
     (dict(k_scale=None), 1, "NULL"), (dict(v_scale=0x10002), 1, "aligned")])
 def test_bad_caches_are_refused(bad, code, word):
     c = _cache(**bad)
