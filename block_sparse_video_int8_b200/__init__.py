@@ -629,6 +629,13 @@ def _stream_of(stream, index: int) -> int:
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+def _on(stream, index: int):
+    """``stream`` as the current one: what a call allocates and clears is then ready for its kernels."""
+    if stream.device_index != index:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the call is on cuda:{index}")
+    return torch.cuda.stream(stream)
+
+
 def _dense(t, dtype, shape, index, name) -> int:
     """The address of a contiguous tensor on device ``index`` (``shape`` None: any)."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous()
@@ -679,6 +686,9 @@ class PagedBatch:
         for n, t in (("q_start", q_start), ("page_table", page_table)):
             if t.device != kv_len.device:
                 raise ValueError(f"{n} is on {t.device}, kv_len is on {kv_len.device}")
+        for n, x, top in (("max_q", max_q, 1 << 24), ("max_kv", max_kv, 1 << 30)):
+            if not 1 <= x <= top:
+                raise ValueError(f"{n} = {x} outside [1, {top}]")
         self._of = (S, int(max_q), int(max_kv), q_start, kv_len, page_table)
         self._index = kv_len.get_device()
         self._refs: dict = {}
@@ -696,6 +706,8 @@ class PagedBatch:
             raise ValueError(f"batch is on cuda:{self._index}, the call is on cuda:{index}")
         r = self._refs.get(T)
         if r is None:
+            if len(self._refs) >= 64:
+                self._refs.clear()
             S, max_q, max_kv, q_start, kv_len, table = self._of
             r = self._refs[T] = ctypes.byref(PagedBatchStruct(S, T, max_q, max_kv, table.shape[1], q_start.data_ptr(),
                                                               kv_len.data_ptr(), table.data_ptr()))
@@ -744,7 +756,7 @@ class PagedKVCache:
                                                0 if k.dtype == torch.int8 else 1, *ptr))
 
     def workspace_bytes(self, batch: PagedBatch, Hq: int, T: int | None = None) -> int:
-        """Bytes for calls of ``T`` packed rows (by default S * max_q) and up to ``Hq`` query heads."""
+        """Bytes for calls of at most ``T`` packed rows (by default S * max_q) and ``Hq`` query heads."""
         n = self._lib.bsva_paged_workspace_bytes(self._ref, batch._ref(batch.S * batch.max_q if T is None else T,
                                                                        self._index), Hq)
         if n == 0:
@@ -761,6 +773,9 @@ class PagedKVCache:
         if torch.cuda.current_device() != index:
             with torch.cuda.device(index):
                 return self.write(k, v, batch, workspace, stream)
+        if stream is not None and workspace is None:
+            with _on(stream, index):
+                return self.write(k, v, batch)
         ks, vs = _tokens(k, self.H, self.d, index, "k"), _tokens(v, self.H, self.d, index, "v")
         T = k.shape[0]
         if v.shape[0] != T:
@@ -780,17 +795,20 @@ class PagedKVCache:
         if torch.cuda.current_device() != index:
             with torch.cuda.device(index):
                 return self.read(batch, first, length, out, workspace, stream)
+        if stream is not None and (out is None or workspace is None):
+            with _on(stream, index):
+                return self.read(batch, first, length, out, workspace)
         S = batch.S
         L = batch.max_kv if length is None else int(length)
         shape = (S, self.H, L, self.d)
         fp = None if first is None else _dense(first, torch.int32, (S,), index, "first")
         if out is None:
-            dev = self.k.device
-            out = (torch.empty(shape, dtype=torch.bfloat16, device=dev), torch.empty(shape, dtype=torch.bfloat16, device=dev))
+            out = (self.k.new_empty(shape, dtype=torch.bfloat16), self.k.new_empty(shape, dtype=torch.bfloat16))
+            kp, vp = out[0].data_ptr(), out[1].data_ptr()
+        else:
+            kp, vp = (_dense(t, torch.bfloat16, shape, index, n) for t, n in zip(out, ("k_out", "v_out"), strict=True))
         ws = torch.zeros(256, dtype=torch.uint8, device=self.k.device) if workspace is None else workspace
-        rc = self._lib.bsva_paged_kv_read(self._ref, batch._ref(0, index), fp, L,
-                                          _dense(out[0], torch.bfloat16, shape, index, "k_out"),
-                                          _dense(out[1], torch.bfloat16, shape, index, "v_out"),
+        rc = self._lib.bsva_paged_kv_read(self._ref, batch._ref(0, index), fp, L, kp, vp,
                                           _dense(ws, torch.uint8, None, index, "workspace"), ws.numel(),
                                           _stream_of(stream, index))
         if rc:
@@ -806,6 +824,11 @@ class PagedKVCache:
         if torch.cuda.current_device() != index:
             with torch.cuda.device(index):
                 return self.attend(q, batch, causal, window, softmax_scale, with_lse, workspace, out, lse, stream)
+        if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
+            with _on(stream, index):
+                return self.attend(q, batch, causal, window, softmax_scale, with_lse, workspace, out, lse)
+        if window > 0x7fffffff:
+            raise ValueError(f"window = {window} is past 2^31 - 1")
         qs = _tokens(q, None, self.d, index, "q")
         T, Hq, d = q.shape
         b = batch._ref(T, index)
@@ -854,6 +877,9 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_len: tor
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             return cross_attn_fwd(q, k, v, k_len, softmax_scale, with_lse, workspace, out, lse, stream)
+    if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
+        with _on(stream, index):
+            return cross_attn_fwd(q, k, v, k_len, softmax_scale, with_lse, workspace, out, lse)
     qp = _dense(q, torch.bfloat16, None, index, "q")
     kv = (s.B, Hkv, s.Lk, s.d)
     kp, vp = _dense(k, torch.bfloat16, kv, index, "k"), _dense(v, torch.bfloat16, kv, index, "v")

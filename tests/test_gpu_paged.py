@@ -1,9 +1,14 @@
 """The paged K/V cache, chunk attention over it and cross attention on the GPU against the fp64 oracle.
 
 Tolerances (u = half a step: 2^-8 bf16, 2^-11 f16, 2^-24 fp32; A = softmax-weighted mean of |v|):
-the output's rounding 2^-8 |o|; each weight's rounding before the second product, 2^-11 A for INT8 values (f16
-weights; one below 2^-14 loses up to 2^-25 of the largest scale: n 2^-24 max|v| covers n of them) and 2^-8 A for
-bf16 values; a logit x of d products in fp32 is off by dx = (d + 4) 2^-24 scale sum|q||k|, which moves a weight by
+the output's rounding 2^-8 |o|; the roundings before the second product:
+ - INT8 values, f16: a weight, a scale and a value times its scale are rounded once each, 3 2^-11 A. What is below
+   2^-14 loses up to 2^-25 instead: a weight that of the largest value, n 2^-24 max|v| for n of them; a value, which
+   enters as code * (s c) / 4096 with s c >= 1 for the largest scale s, 2^-25 4096 s <= 2^-13 max|v| / 127 < 2^-19 max|v|,
+   times weights that sum to 1.
+ - bf16 values: a weight p enters as p (1 + e), |e| <= 2^-8, and the sum that divides as it entered, so that o moves by
+   sum p e (v - o) / sum p (1 + e), at most 2^-8 (A + |o|) (1 + 2^-7).
+A logit x of d products in fp32 is off by dx = (d + 4) 2^-24 scale sum|q||k|, which moves a weight by
 the factor 1 +- 2 dx and so o by 2 dx 2 A; the exponential and the fp32 sums over n keys add (n + 8) 2^-22 A.
 lse: dx + (n + 8) 2^-22 + 2^-22 |lse|.
 """
@@ -110,10 +115,12 @@ def close(q, k, v, ok, o, lse, scale, dtype, where):
     keys = max(1, ok.shape[1])
     dx = ((d + 4) * 2.0 ** -24 * sc * np.where(ok, np.abs(q) @ np.abs(k).T, 0).max(1, initial=0))[:, None]
     vmax = np.abs(np.where(ok.any(0)[:, None], v, 0)).max(initial=0)
-    u = 2.0 ** -11 if dtype == torch.int8 else 2.0 ** -8
+    u = 3 * 2.0 ** -11 if dtype == torch.int8 else 2.0 ** -8
     tol = 2.0 ** -8 * np.abs(ro) + (u + 4 * dx + (keys + 8) * 2.0 ** -22) * A * 1.01 + 1e-38
     if dtype == torch.int8:
-        tol += keys * 2.0 ** -24 * vmax
+        tol += (keys * 2.0 ** -24 + 2.0 ** -19) * vmax
+    else:
+        tol += 2.0 ** -8 * np.abs(ro)
     bad = ~(np.abs(o - ro) <= tol)
     assert not bad.any(), f"{where}: {bad.sum()} of {bad.size}, worst {np.nanmax(np.abs(o - ro) / tol)} of the bound"
     dead = ~np.isfinite(rl)
@@ -468,3 +475,194 @@ def test_cross_attention(gpu_lib, B, Hq, Hkv, Lq, Lk, d):
                 hk = h // (Hq // Hkv)
                 close(q[b, h].double().numpy(), k[b, hk, :n].double().numpy(), v[b, hk, :n].double().numpy(),
                       np.ones((Lq, n), bool), o[b, h], ls[b, h], None, torch.bfloat16, f"batch {b} head {h}")
+
+
+# ------------------------------------------------------------------ loose bounds, many heads, repeated pages, no work
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("max_q,max_kv", [(8, 4096), (500, 4096), (500, 100000)])
+def test_bounds_far_above_the_lengths(gpu_lib, dtype, max_q, max_kv):
+    # the launch follows the bounds: splits and row tiles without work; entries without tokens or pages
+    lens = [(1, 70), (0, 0), (8, 8), (3, 200), (0, 40)]
+    st = Setup(gpu_lib, lens, 2, 64, 16, dtype, seed=71, lead=3, tail=4)
+    table = torch.full((len(lens), -(-max_kv // 16)), -1, dtype=torch.int32, device="cuda")
+    table[:, :st.table.shape[1]] = st.batch.page_table
+    st.batch = gpu_lib.PagedBatch(st.batch.q_start, st.batch.kv_len, table, max_q, max_kv)
+    _attend(st, 6)
+    _attend(st, 6, window=50)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("G", [33, 71, 128, 192])
+@pytest.mark.parametrize("n", [1, 3])
+def test_many_query_heads_a_key_head(gpu_lib, dtype, G, n):
+    _attend(Setup(gpu_lib, [(n, 300), (1, 17)], 1, 64, 32, dtype, seed=G), G)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 70])
+def test_a_page_twice_in_a_table(gpu_lib, dtype, n):
+    st = Setup(gpu_lib, [(n, 200), (n, 130)], 2, 128, 32, dtype, seed=81)
+    table = st.table.copy()
+    table[0, 1] = table[0, 0]
+    st.batch.page_table.copy_(torch.from_numpy(table))
+    for z in range(2):
+        st.values[z][0][32:64] = st.values[z][0][:32]
+    _attend(st, 4)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 100])
+def test_windows_as_long_as_the_sequences_are_none(gpu_lib, dtype, n):
+    st = Setup(gpu_lib, [(n, 400), (n, n), (n, n // 2)], 2, 64, 16, dtype, seed=91)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(4).cuda()
+    a, la = st.cache.attend(q, st.batch, with_lse=True)
+    for window in (400, 2 ** 30, 2 ** 31 - 1):
+        b, lb = st.cache.attend(q, st.batch, window=window, with_lse=True)
+        assert torch.equal(a[:2 * n], b[:2 * n]) and torch.equal(la[:2 * n], lb[:2 * n])
+        assert torch.equal(torch.isinf(la), torch.isinf(lb))
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+def test_nothing_to_do(gpu_lib, dtype):
+    st = Setup(gpu_lib, [(0, 20), (0, 0)], 2, 64, 16, dtype, seed=101, tail=2)
+    ws = st.cache.new_workspace(st.batch, 4, st.T)
+    _attend(st, 4)                                   # two rows, of no sequence: left as they were
+    q = torch.zeros((0, 4, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = st.cache.attend(q, st.batch, with_lse=True, workspace=ws)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    st.cache.write(q[:, :2], q[:, :2], st.batch, workspace=ws)
+    k, v = st.cache.read(st.batch, first=torch.tensor([20, 0], dtype=torch.int32, device="cuda"), length=5, workspace=ws)
+    gpu_lib.check_status(ws)
+    assert (k == 0).all() and (v == 0).all()
+
+
+def test_binding_refusals(gpu_lib):
+    st = Setup(gpu_lib, [(1, 20)], 2, 64, 16, torch.int8, seed=5)
+    b, q = st.batch, st.queries(4).cuda()
+    for max_q, max_kv in ((0, 20), (2 ** 32 + 1, 20), (1, 0), (1, 2 ** 33)):
+        with pytest.raises(ValueError, match="max_"):
+            gpu_lib.PagedBatch(b.q_start, b.kv_len, b.page_table, max_q, max_kv)
+    with pytest.raises(ValueError, match="window"):
+        st.cache.attend(q, b, window=2 ** 32 + 1)
+    with pytest.raises(gpu_lib.BsvaError, match="window"):
+        st.cache.attend(q, b, window=-1)
+    with pytest.raises(ValueError, match="shape"):
+        st.cache.read(b, out=(q, q))
+    with pytest.raises(TypeError):
+        st.cache.attend(q.half(), b)
+    with pytest.raises(ValueError, match="strides"):
+        st.cache.attend(torch.zeros((1, 64, 4), dtype=torch.bfloat16, device="cuda").transpose(1, 2), b)
+    with pytest.raises(ValueError, match="tokens"):
+        st.cache.write(st.new[0], torch.cat([st.new[1], st.new[1]]), b)
+    with pytest.raises(gpu_lib.BsvaError, match="workspace"):
+        st.cache.attend(q, b, workspace=torch.zeros(255, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(gpu_lib.BsvaError, match="multiple"):
+        st.cache.attend(q[:, :3], b)
+
+
+# ------------------------------------------------------------------------------- streams, graphs, calls at once
+def _call_kinds(gpu_lib, seed):
+    """A single-token call, a chunk over each kind of cache and a cross attention, as functions of their workspace."""
+    kinds = []
+    for dtype, lens, Hq in ((torch.int8, [(1, 900), (1, 40)], 8), (torch.int8, [(150, 700), (90, 90)], 2),
+                            (torch.bfloat16, [(150, 700), (90, 90)], 2), (torch.bfloat16, [(1, 900), (1, 40)], 8)):
+        st = Setup(gpu_lib, lens, 2, 64, 16, dtype, seed=seed)
+        q = st.queries(Hq).cuda()
+        st.cache.write(st.new[0], st.new[1], st.batch)
+
+        def call(st=st, q=q, **kw):
+            st.cache.write(st.new[0], st.new[1], st.batch, **kw)
+            k, v = st.cache.read(st.batch, **kw)
+            return (*st.cache.attend(q, st.batch, with_lse=True, **kw), k, v)
+        kinds.append((call, st.cache.new_workspace(st.batch, Hq, st.T)))
+    rng = np.random.default_rng(seed)
+    for Lq in (3, 200):
+        q, k, v = (_bf16(rng, (2, 4, L, 64)).cuda() for L in (Lq, 301, 301))
+        kinds.append((lambda q=q, k=k, v=v, **kw: gpu_lib.cross_attn_fwd(q, k, v, with_lse=True, **kw),
+                      gpu_lib.new_cross_attn_workspace(q, k)))
+    return kinds
+
+
+def test_given_stream_orders_what_the_call_allocates(gpu_lib):
+    # on a stream that is busy, without workspace or outputs: what the call clears is cleared before its kernels
+    side, busy = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    for call, ws in _call_kinds(gpu_lib, 111):
+        want = call(workspace=ws)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                busy = busy @ busy * 1e-2
+        got = call(stream=side)
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(stream=side, workspace=ws)
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_calls_at_once_on_two_streams(gpu_lib):
+    kinds = [_call_kinds(gpu_lib, 121), _call_kinds(gpu_lib, 122)]
+    want = [[call(workspace=ws) for call, ws in ks] for ks in kinds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [[], []]
+        for i in range(len(kinds[0])):
+            for z in range(2):
+                j = i if z == 0 else len(kinds[0]) - 1 - i
+                with torch.cuda.stream(streams[z]):
+                    got[z].append((j, kinds[z][j][0](workspace=kinds[z][j][1])))
+        torch.cuda.synchronize()
+        for z in range(2):
+            for j, g in got[z]:
+                gpu_lib.check_status(kinds[z][j][1])
+                assert all(torch.equal(x, y) for x, y in zip(g, want[z][j]))
+
+
+def test_two_graphs_replayed_in_turn_and_at_once(gpu_lib):
+    kinds = [_call_kinds(gpu_lib, 131), _call_kinds(gpu_lib, 132)]
+    want = [[call(workspace=ws) for call, ws in ks] for ks in kinds]
+    graphs, got = [], []
+    for ks in kinds:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append([call(workspace=ws) for call, ws in ks])
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for at_once in (False, True, True):
+        for outs in got:
+            for o in outs:
+                for x in o:
+                    x.fill_(3)
+        torch.cuda.synchronize()
+        for z in range(2):
+            with torch.cuda.stream(streams[z if at_once else 0]):
+                graphs[z].replay()
+        torch.cuda.synchronize()
+        for z in range(2):
+            for (_, ws), g, w in zip(kinds[z], got[z], want[z]):
+                gpu_lib.check_status(ws)
+                assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+def test_two_graphs_with_one_workspace_in_turn(gpu_lib):
+    # graphs that share a workspace may follow each other on a stream: nothing is kept in it from one call for the next
+    a, b = _call_kinds(gpu_lib, 141), _call_kinds(gpu_lib, 142)
+    ws = torch.zeros(max(w.numel() for _, w in a + b), dtype=torch.uint8, device="cuda")
+    want = [[call(workspace=ws) for call, _ in ks] for ks in (a, b)]
+    graphs, got = [], []
+    for ks in (a, b):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append([call(workspace=ws) for call, _ in ks])
+        graphs.append(g)
+    for z in (0, 1, 1, 0):
+        graphs[z].replay()
+    gpu_lib.check_status(ws)
+    for z in range(2):
+        for g, w in zip(got[z], want[z]):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
