@@ -232,8 +232,10 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
     return it.nh > 0;
   };
 
-  // Registers go to the softmax. INT8, 512 threads with 128 each: 2 x 168 + 56 + 120 = 4 x 128 for the four warpgroups;
-  // bf16, 384 threads with 168 each: 2 x 184 + 136 = 2 x 192 + 120 = 3 x 168, with which nothing is spilled.
+  // Registers go to the softmax. INT8, 512 threads with 128 each: 2 x 168 + 64 + 112 = 4 x 128 for the four warpgroups
+  // (2048 x 32760 tokens, us: 2054; 56 and 120 for the last two 2070; 2 x 176 + 56 + 104 2079; 2 x 160 + 72 + 120 2130).
+  // bf16, 384 threads with 168 each: 2 x 184 + 136 = 2 x 192 + 120 = 3 x 168, with which nothing is spilled. (A fourth
+  // warpgroup for the output leaves the others too few: 32760 x 512 tokens, 40 heads, 446 us for 393.)
   if (warp < 8) {
     regs_up<I8 ? 168 : LSE ? 192 : 184>();
     // --------------------------------------------------------------------------------------- softmax
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
     }
   } else if (warp >= 12) {
     if constexpr (I8) {
-      regs_down<120>();
+      regs_down<112>();
       // ---------------------------------------------------------------------------- key tiles, INT8 codes
       const int lt = tid - 384;
       constexpr int CPR = D / 16, RP = 128 / CPR, NP = KT / RP;   // 16-byte pieces a row, rows a pass, passes
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       }
     }
   } else {
-    regs_down<I8 ? 56 : LSE ? 120 : 136>();
+    regs_down<I8 ? 64 : LSE ? 120 : 136>();
     if (warp == 11) {
       // ------------------------------------------------------------------------------------- next item
       int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z;
