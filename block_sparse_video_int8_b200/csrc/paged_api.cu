@@ -9,7 +9,7 @@ using namespace bsva;
 
 namespace {
 
-constexpr int kMaxSplits = 64;
+constexpr int kMaxSplits = 256;
 
 int ilog2(int x) {
   int r = 0;
@@ -96,14 +96,15 @@ Plan make_plan(int S, int Hkv, int G, int max_q, int keys, int d, bool int8) {
     return p;
   }
   const long long nr = rows <= 8 ? 8 : 16, items = (rows + nr - 1) / nr * Hkv * S;
-  // Three CTAs an SM run at once. Splits of 128 keys (two blocks a warp) until they are filled once, of 512 keys until
-  // four times: short ends and unequal sequences then leave few SMs idle, and joining costs little beside 512 keys.
-  // (One, four, eight times, us: 2 x 131000 keys 550, 433, 443; 16 sequences of up to 1500 keys 21, 24.6, 26.7.)
+  // Three CTAs an SM run at once. Splits of 128 keys (two blocks a warp) until they are filled once, of 1024 keys until
+  // four times: short ends and unequal sequences then leave few SMs idle, and joining costs little beside 1024 keys.
+  // (One, four, eight times, us: 2 x 131000 keys, 40 key heads 550, 433, 443; 16 sequences of up to 1500 keys 21, 24.6,
+  // 26.7. Least keys 512, 1024: 32768 keys, 8 key heads 34, 30; 131000 86, 82; 4 x 5000 23.3, 21.8.)
   auto splits = [&](long long ctas, long long least) {
     const long long want = (ctas + items - 1) / items, most = (keys + least - 1) / least;
     return want < most ? want : most;
   };
-  long long n = splits(148 * 3, 128), n4 = splits(148 * 12, 512);
+  long long n = splits(148 * 3, 128), n4 = splits(148 * 12, 1024);
   n = n > n4 ? n : n4;
   n = n < kMaxSplits ? n : kMaxSplits;
   n = n < 1 ? 1 : n;

@@ -450,33 +450,55 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   }
 }
 
-// Joins the splits of every output row, in their order. One group of D/4 lanes a row, 4 values a lane.
-template <int D>
+// Joins the splits of every output row, in an order that the number of splits fixes. PG groups of D/4 lanes a row, 4
+// values a lane; group g takes splits g, g + PG, ... and the groups' sums are joined in shared memory.
+template <int D, int PG>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
-  constexpr int LPR = D / 4;
+  constexpr int LPR = D / 4, RPB = 256 / (LPR * PG);
   // launched while the kernel that writes the parts still runs: from here on its results are there
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long x = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;   // (token, head) of the sequence
-  const int c = threadIdx.x % LPR;
+  const int c = threadIdx.x % LPR, g = threadIdx.x / LPR % PG, rw = threadIdx.x / (LPR * PG);
+  const long long x = (long long)blockIdx.x * RPB + rw;   // (token, head) of the sequence
   const int s = blockIdx.y, Hq = a.Hkv * a.G;
   const SeqView sv = seq_view(a, s);
-  if (x >= (long long)sv.n * Hq) return;
-  const long long off = (long long)s * a.o_seq + (sv.q0 + x / Hq) * a.o_tok + (x % Hq) * a.o_head;
+  const bool in = x < (long long)sv.n * Hq;
+  const long long off = in ? (long long)s * a.o_seq + (sv.q0 + x / Hq) * a.o_tok + (x % Hq) * a.o_head : 0;
   const size_t row = off / D;
-  float mx = -INFINITY;
-  for (int p = 0; p < a.nsplit; ++p) mx = fmaxf(mx, a.part_ml[size_t(p) * a.out_rows + row].x);
-  float ls = 0.f, le = 0.f;
+  float mx = -INFINITY, ls = 0.f, le = 0.f;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < a.nsplit; ++p) {
-    const size_t pr = size_t(p) * a.out_rows + row;
-    const float4 ml = a.part_ml[pr];
-    if (ml.x == -INFINITY) continue;   // a split without a key of this row: its output part is not written
-    const float f = ex2_approx(ml.x - mx);
-    const float4 z = *reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c);
-    ls += f * ml.y;
-    le += f * ml.z;
-    y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
+  if (in) {
+    for (int p = g; p < a.nsplit; p += PG) mx = fmaxf(mx, a.part_ml[size_t(p) * a.out_rows + row].x);
+    for (int p = g; p < a.nsplit; p += PG) {
+      const size_t pr = size_t(p) * a.out_rows + row;
+      const float4 ml = a.part_ml[pr];
+      if (ml.x == -INFINITY) continue;   // a split without a key of this row: its output part is not written
+      const float f = ex2_approx(ml.x - mx);
+      const float4 z = *reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c);
+      ls += f * ml.y;
+      le += f * ml.z;
+      y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
+    }
   }
+  if constexpr (PG > 1) {
+    __shared__ float4 s_y[RPB][PG][LPR], s_ml[RPB][PG];
+    s_y[rw][g][c] = y;
+    if (c == 0) s_ml[rw][g] = make_float4(mx, ls, le, 0.f);
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 0; i < PG; ++i) mx = fmaxf(mx, s_ml[rw][i].x);
+    ls = le = 0.f;
+    y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < PG; ++i) {
+      const float4 ml = s_ml[rw][i], z = s_y[rw][i][c];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+      ls += f * ml.y;
+      le += f * ml.z;
+      y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
+    }
+  }
+  if (!in) return;
   const float inv = ls > 0.f ? 1.f / ls : 0.f;
   *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
       make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
@@ -507,7 +529,12 @@ cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st) {
 }
 
 cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st) {
-  const long long rows = (long long)a.max_q * a.Hkv * a.G, rpb = 256 / (a.d / 4);
+  const long long rows = (long long)a.max_q * a.Hkv * a.G;
+  // Eight groups a row shorten the chain of loads, which is all there is to few rows: 40 rows of 8 splits 13.3 us with
+  // the kernel before it (one group 15.4), of 64 splits 19.5 (34), of 222 117 (229). Many rows of few splits
+  // keep the GPU busy with one group: 4096 rows of 9 splits, 265 us for 271.
+  const int pg = a.nsplit > 16 || (a.nsplit > 2 && rows * a.S <= 2048) ? 8 : 1;
+  const long long rpb = 256 / (a.d / 4 * pg);
   // the launch overlaps the end of the kernel before it (the parts' writer); the device waits for that one itself
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -518,8 +545,9 @@ cudaError_t launch_paged_combine(const PagedArgs& a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return a.d == 128 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, a)
-                    : cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, a);
+  auto go = [&](auto f) { return cudaLaunchKernelEx(&cfg, f, a); };
+  if (a.d == 128) return pg > 1 ? go(paged_combine_kernel<128, 8>) : go(paged_combine_kernel<128, 1>);
+  return pg > 1 ? go(paged_combine_kernel<64, 8>) : go(paged_combine_kernel<64, 1>);
 }
 
 }  // namespace bsva
