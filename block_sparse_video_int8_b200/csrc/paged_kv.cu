@@ -5,9 +5,11 @@
 // 0 where s = 0: the library's block quantiser with the block shrunk to one row, so that a token can be
 // appended without touching the codes of its neighbours. Reading gives bf16(code * s).
 //
-// Both kernels move every byte once and are bound by HBM: writing takes 2 B in and 1 + 4/d B out an element,
-// reading the reverse. A row of d values is held by d/8 lanes (16 bytes of bf16 each), so a warp's loads
-// and stores are whole 32-byte sectors; each thread has several independent rows in flight.
+// Both kernels move every byte once: writing takes 2 B in and 1 + 4/d B out an element, reading the reverse. A row of
+// d values is held by d/8 lanes (16 bytes of bf16 each), so a warp's loads and stores are whole 32-byte sectors; each
+// thread has several independent rows in flight. Measured, 2 sequences of 8064 tokens, 40 heads of 128 (d = 64 within
+// 5 % for the same bytes): bf16 pages, write 109 us (6.05 TB/s of a measured copy's 6.54), read 106 (6.2); INT8 pages,
+// read 84 us (6.0), bound by HBM like those; write 130 us (3.85), bound by the quantiser's instructions.
 #include "common.cuh"
 #include "paged.cuh"
 #include "quant.cuh"
@@ -31,11 +33,16 @@ __device__ __forceinline__ uint2 quant8(const uint32_t (&w)[4], float sc, float 
     const float2 d = __ffma2_rn(__fadd2_rn(t[e], nmg), n1, q);   // exact: how far q is from its integer
     asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(dm) : "f"(dm), "f"(d.x), "f"(d.y));
   }
-  // near a half-integer, or a scale below 2^-120 (its reciprocal could overflow): the IEEE division
+  // near a half-integer, or a scale below 2^-120 (its reciprocal could overflow): the IEEE division. Half of the warps
+  // come here, since half a row's largest value, 63.5 s, is a common one, so the pairs are looked at once more
+  // (2 x 8064 tokens, 40 heads: 130 us, all four pairs divided 139, none 107).
   if (dm >= kBand || (sc > 0.f && rcp == 0.f)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      t[e] = make_float2(quant_exact(__uint_as_float(w[e] << 16), sc), quant_exact(__uint_as_float(w[e] & 0xFFFF0000u), sc));
+    for (int e = 0; e < 4; ++e) {
+      const float x = __uint_as_float(w[e] << 16), y = __uint_as_float(w[e] & 0xFFFF0000u);
+      if (rcp == 0.f || fabsf(x * rcp - (t[e].x - kMagic)) >= kBand || fabsf(y * rcp - (t[e].y - kMagic)) >= kBand)
+        t[e] = make_float2(quant_exact(x, sc), quant_exact(y, sc));
+    }
   }
   uint32_t b[4];
 #pragma unroll
