@@ -803,7 +803,8 @@ class PagedKVCache:
         shape = (S, self.H, L, self.d)
         fp = None if first is None else _dense(first, torch.int32, (S,), index, "first")
         if out is None:
-            out = (self.k.new_empty(shape, dtype=torch.bfloat16), self.k.new_empty(shape, dtype=torch.bfloat16))
+            k_out = self.k.new_empty(shape, dtype=torch.bfloat16)
+            out = (k_out, torch.empty_like(k_out))
             kp, vp = out[0].data_ptr(), out[1].data_ptr()
         else:
             kp, vp = (_dense(t, torch.bfloat16, shape, index, n) for t, n in zip(out, ("k_out", "v_out"), strict=True))
@@ -886,16 +887,20 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_len: tor
     lp = None if k_len is None else _dense(k_len, torch.int32, (s.B,), index, "k_len")
     rows = (s.B, s.H, s.Lq)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _dense(out, torch.bfloat16, q.shape, index, "out")
     if with_lse and lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+        lse = q.new_empty(rows, dtype=torch.float32)
+        ep = lse.data_ptr()
+    else:
+        ep = None if lse is None else _dense(lse, torch.float32, rows, index, "lse")
     if workspace is None:
         workspace = new_cross_attn_workspace(q, k)
-    lib = load()
-    rc = lib.cross_attn_fwd(s, Hkv, qp, kp, vp, lp, softmax_scale, _dense(out, torch.bfloat16, q.shape, index, "out"),
-                            None if lse is None else _dense(lse, torch.float32, rows, index, "lse"),
-                            _dense(workspace, torch.uint8, None, index, "workspace"), workspace.numel(),
-                            _stream_of(stream, index))
+    rc = load().cross_attn_fwd(s, Hkv, qp, kp, vp, lp, softmax_scale, op, ep,
+                               _dense(workspace, torch.uint8, None, index, "workspace"), workspace.numel(),
+                               _stream_of(stream, index))
     if rc:
         _check(rc)
     return (out, lse) if with_lse else out
