@@ -19,6 +19,9 @@
 //   consecutive d values a step; of V it reads 1/8 of the d values of tile rows 2t, 2t+1, 2t+8, 2t+9.
 // Tile row g is key g or, odd, key g ^ 4, and pieces of a row are stored exclusive-or its number: eight
 // lanes that read together then meet eight different banks, for K and for V.
+// Measured, one token of each sequence, heads of 128 (a copy moves 6.54 TB/s): 64 sequences of 8192 keys, 8 key heads,
+// bf16 pages 323 us (6.66 TB/s), INT8 pages 196 (5.66; issue slots 56 % taken by widening and the softmax, MUFU 5 %);
+// 2 of 131000 keys, 40 key heads, INT8 458 (6.0). The codes through registers instead of the rings took 537 of 458.
 
 #include <climits>
 
