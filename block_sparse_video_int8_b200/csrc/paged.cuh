@@ -37,6 +37,7 @@ struct PagedArgs {
   int causal, window;
   int q_tma;                    // tile kernel: Q by TMA (G divides 128)
   int nsplit, split_keys;       // rows kernel: keys of a split; tile kernel: splits share a row tile's key tiles
+  int cluster;                  // rows kernel: the splits of a row tile are a cluster of CTAs, which joins them
   uint64_t wait_limit_ns;
 };
 

@@ -63,6 +63,7 @@ int check_heads(int Hq, int Hkv, long long max_q) {
 struct Plan {
   bool tiles = false;   // tensor-core tiles of 256 rows, or 8 or 16 rows a CTA
   int nsplit = 1, split_keys = 0;
+  bool cluster = false;   // the splits of a row tile are a cluster of CTAs, which joins them without a second kernel
   int cap = 1;   // >= nsplit, and no smaller for more keys: workspaces are sized by it
 };
 
@@ -112,6 +113,10 @@ Plan make_plan(int S, int Hkv, int G, int max_q, int keys, int d, bool int8) {
   const long long per = ((keys + n - 1) / n + 63) / 64 * 64;
   p.split_keys = int(per);
   p.nsplit = int((keys + per - 1) / per);
+  // A cluster of 8 at most joins its splits itself where each CTA has an SM to itself: one launch less, 1003 keys, 8 key
+  // heads (64 CTAs) 8.3 us a call in a loop for 9.8. Where SMs hold several CTAs, those that wait for their cluster
+  // keep others out: 16 sequences of 1500 keys, 12 heads (576 CTAs) 16.5 us for 14.5; 8 x 3000 keys, 8 heads 32.8 for 27.6.
+  p.cluster = p.nsplit > 1 && p.nsplit <= 8 && items * p.nsplit <= 148;
   return p;
 }
 
@@ -140,6 +145,7 @@ int run_paged(PagedArgs& a, bool int8, const Plan& p, const PagedWs& w, void* wo
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.nsplit = p.nsplit;
   a.split_keys = p.split_keys;
+  a.cluster = p.cluster;
   a.part_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr;
   a.part_ml = p.nsplit > 1 ? reinterpret_cast<float4*>(ws + w.part_ml) : nullptr;
   PagedMaps maps{};
@@ -162,7 +168,7 @@ int run_paged(PagedArgs& a, bool int8, const Plan& p, const PagedWs& w, void* wo
   }
   cudaError_t e = p.tiles ? launch_paged_tiles(a, maps, int8, st) : launch_paged_rows(a, int8, st);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-  if (p.nsplit > 1) {
+  if (p.nsplit > 1 && !a.cluster) {
     e = launch_paged_combine(a, st);
     if (e != cudaSuccess) return cuda_fail(e, "split combination launch");
   }

@@ -74,6 +74,29 @@ constexpr int kRowSmem() {
   return ring > join ? ring : join;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Where a variable of this CTA's shared memory lies in that of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* p, int rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 template <int D, bool I8, int NT>
 __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs a) {
   constexpr int KS = D / 16;              // steps of 16 d values in q . k
@@ -95,8 +118,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   const int past = sv.kv - sv.n;
   const int hi_all = a.causal ? min(sv.kv, past + i1 + 1) : sv.kv;
   const int lo_see = a.window ? max(0, past + i0 - a.window + 1) : 0, lo_all = lo_see & ~15;
-  const int lo = min((long long)lo_all + (long long)sp * a.split_keys, (long long)INT_MAX - 64);
-  const int hi = min((long long)hi_all, (long long)lo + a.split_keys);
+  // (a cluster shares what there is: its CTAs wait for one another at the end)
+  const int per = a.cluster ? ((max(hi_all - lo_all, 0) + a.nsplit - 1) / a.nsplit + 63) & ~63 : a.split_keys;
+  const int lo = min((long long)lo_all + (long long)sp * per, (long long)INT_MAX - 64);
+  const int hi = min((long long)hi_all, (long long)lo + per);
 
   // this lane's rows as columns of the products: 8 nt + 2t and + 1; what each sees
   int see_lo[NT][2], see_hi[NT][2];       // first and last key
@@ -397,6 +422,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   // ---- join the four warps: each leaves its maximum, sum and output (over cn) in shared memory
   constexpr int W = kRowThreads / 32, NR = 8 * NT;
   __shared__ float s_m[W][NR], s_l[W][NR];
+  __shared__ float2 s_ml[NR];             // of the CTA, for its cluster
   float (*s_o)[NR][D + 4] = reinterpret_cast<float (*)[NR][D + 4]>(smem_rows);   // over the rings, which are through
   __syncthreads();
   const float inv_c = I8 && cn != 0.f ? 1.f / cn : 1.f;
@@ -440,7 +466,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
     const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
                           (long long)(h * a.G + rr % a.G) * a.o_head;
-    if (a.nsplit > 1) {
+    if (a.cluster) {
+      *reinterpret_cast<float4*>(&s_o[0][r][4 * c]) = y;
+      if (c == 0) s_ml[r] = make_float2(mx, ls);
+    } else if (a.nsplit > 1) {
       const size_t pr = size_t(sp) * a.out_rows + off / D;
       *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c) = y;
       if (c == 0) a.part_ml[pr] = make_float4(mx, ls, ls, 0.f);
@@ -451,6 +480,31 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       if (c == 0 && a.lse) a.lse[off / D] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
     }
   }
+  if (!a.cluster) return;
+  // ---- join the cluster: each of its CTAs takes a share of the outputs and reads the others' parts, in their order
+  cluster_sync();
+  for (int x = sp * kRowThreads + threadIdx.x; x < NR * (D / 4); x += a.nsplit * kRowThreads) {
+    const int r = x / (D / 4), c = x % (D / 4);
+    const int rr = rb + r;
+    if (rr >= R) continue;
+    float mx = -INFINITY, ls = 0.f;
+    for (int p = 0; p < a.nsplit; ++p) mx = fmaxf(mx, ld_cluster2(in_cta(&s_ml[r], p)).x);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < a.nsplit; ++p) {
+      const float2 ml = ld_cluster2(in_cta(&s_ml[r], p));
+      const float4 z = ld_cluster4(in_cta(&s_o[0][r][4 * c], p));
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+      ls += f * ml.y;
+      y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
+    }
+    const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
+                          (long long)(h * a.G + rr % a.G) * a.o_head;
+    const float inv = ls > 0.f ? 1.f / ls : 0.f;
+    *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
+        make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+    if (c == 0 && a.lse) a.lse[off / D] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+  }
+  cluster_sync();                         // no CTA leaves while another reads its parts
 }
 
 // Joins the splits of every output row, in an order that the number of splits fixes. PG groups of D/4 lanes a row, 4
@@ -517,7 +571,19 @@ cudaError_t launch_paged_rows(const PagedArgs& a, bool int8, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   auto go = [&](auto f, int smem) {
     if (smem > 40 * 1024) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) f<<<grid, kRowThreads, smem, st>>>(a);
+    if (e != cudaSuccess) return;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = unsigned(a.nsplit);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = kRowThreads;
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.cluster ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, f, a);
   };
 #define BSVA_ROWS(D, I8)                                              \
   nr == 8 ? go(paged_rows_kernel<D, I8, 1>, kRowSmem<D, I8, 1>())     \
