@@ -897,6 +897,9 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
+    // after a wait that ran out, copies and products may still be on their way into this CTA's memory: 100 us for them
+    if (*abort)
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 100000;) __nanosleep(1000);
     tc_fence_after();
     tmem_dealloc(tmem, kTileTmem);
   }
