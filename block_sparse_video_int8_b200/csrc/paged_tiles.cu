@@ -85,8 +85,8 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
                : "memory");
 }
 
@@ -399,7 +399,10 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           ahead = done;
           if (late) publish(0);
           if ((I8 || looked) && __any_sync(0xffffffffu, f != 1.f) && !(alive = rescale(sub))) break;
-          if (!done) {
+          if (!done && __all_sync(0xffffffffu, clo > col + 63 || chi < col)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = 0;   // no row of the warp sees any of the 64 keys
+          } else if (!done) {
             // scaled logits of 32 columns in xa, -inf where the row does not see. They are rounded before the maximum is
             // taken off (fused, those past 2^24 would come out above it by half their own step), so the largest is
             // exactly 0.
@@ -678,9 +681,13 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         if (more) {
           it.s = z;
           it.h = y;
-          it.sp = x % a.nsplit;
           // the last rows of a causal chunk have the most keys: they start first
-          it.rb = (int(gridDim.x) / a.nsplit - 1 - x / a.nsplit) * 256;
+          it.sp = 0;
+          it.rb = (int(gridDim.x) - 1 - x) * 256;
+          if (a.nsplit > 1) {
+            it.sp = x % a.nsplit;
+            it.rb = (int(gridDim.x) / a.nsplit - 1 - x / a.nsplit) * 256;
+          }
           const SeqView sv = seq_view(a, it.s);
           it.R = sv.n * a.G;
           it.kv = sv.kv;
@@ -693,9 +700,12 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
             it.lo_all = a.window ? max(0, it.past + it.rb / a.G - a.window + 1) : 0;
             it.t0 = it.lo_all / KT;
             if (hi > it.lo_all) {
-              const int all = (hi + KT - 1) / KT - it.t0, per = (all + a.nsplit - 1) / a.nsplit;
-              it.t0 += it.sp * per;
-              it.N = max(0, min(per, all - it.sp * per));
+              it.N = (hi + KT - 1) / KT - it.t0;
+              if (a.nsplit > 1) {
+                const int per = (it.N + a.nsplit - 1) / a.nsplit;
+                it.t0 += it.sp * per;
+                it.N = max(0, min(per, it.N - it.sp * per));
+              }
             }
           }
         }
@@ -725,16 +735,31 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       // --------------------------------------------------------------------------------------------- Q
       constexpr int CPR = D / 8, RP = 32 * kQWarps / CPR;
       const int qt = tid - (I8 ? 288 : 320), c = qt % CPR, r0 = qt / CPR;
-      const int di = RP / a.G, dg = RP % a.G;
+      static_assert(RP == 2 || RP == 4 || RP == 8, "rows within a swizzle atom");
+      const int dg = RP % a.G;                     // RP rows on: step elements, and wrap more where the heads begin anew
+      const long long step = RP / a.G * a.q_tok + dg * a.q_head, wrap = a.q_tok - a.G * a.q_head;
       Item it;
       uint32_t used[2] = {0, 0};
       bool ok = true;
       for (uint32_t no = 0; ok && take(it, no, true); ++no) {
         if (it.N == 0) continue;
+        auto ready = [&]() {                     // this warp's rows of the halves that were committed
+          fence_proxy_async_smem();
+          __syncwarp();
+        };
+        bool held = false;                       // half 0 is on its way and not reported yet
   #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           if (hf >= it.nh || !ok) break;
-          if (used[hf] > 0 && !(ok = wait_idle(&sm.q_empty[hf], used[hf] - 1))) break;
+          if (used[hf] > 0) {
+            if (held && !__all_sync(0xffffffffu, mbar_test_wait(&sm.q_empty[hf], (used[hf] - 1) & 1))) {
+              asm volatile("cp.async.wait_group 0;" ::: "memory");
+              ready();
+              if (lane == 0) mbar_arrive(&sm.q_full[0]);
+              held = false;
+            }
+            if (!(ok = wait_idle(&sm.q_empty[hf], used[hf] - 1))) break;
+          }
           ++used[hf];
           if (a.q_tma) {                         // a box of G heads and 128 / G tokens a panel, by the first of the warps
             if (lane == 0) {
@@ -750,28 +775,38 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
             __syncwarp();
             continue;
           }
-          int rr = it.rb + hf * 128 + r0;
-          int i = rr / a.G, g = rr % a.G;
-          const __nv_bfloat16* base = a.q + (long long)it.s * a.q_seq + (long long)it.q0 * a.q_tok +
-                                      (long long)(it.h * a.G) * a.q_head + c * 8;
-  #pragma unroll 4
-          for (int r = r0; r < 128; r += RP) {     // zeros behind the last row
-            const bool in = rr < it.R;
-            cp_async16(chunk_at<D>(sm.q[hf], r, c), in ? base + (long long)i * a.q_tok + (long long)g * a.q_head : a.q, in);
-            rr += RP;
-            i += di;
+          const int first = it.rb + hf * 128 + r0;
+          int g = first % a.G;
+          const __nv_bfloat16* from = a.q + (long long)it.s * a.q_seq + (long long)(it.q0 + first / a.G) * a.q_tok +
+                                      (long long)(it.h * a.G + g) * a.q_head + c * 8;
+          const uint32_t to = smem_u32(chunk_at<D>(sm.q[hf], r0, c));
+  #pragma unroll 8
+          for (int n = 0; n < 128 / RP; ++n) {     // row r0 + n RP of the half; zeros behind the last row
+            const bool in = first + n * RP < it.R;
+            cp_async16((to ^ (n * RP % 8 * 16)) + n * RP * 128, in ? from : a.q, in);
+            from += step;
             g += dg;
             if (g >= a.G) {
               g -= a.G;
-              ++i;
+              from += wrap;
             }
           }
-          asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (hf == 0 && it.nh == 2) {             // half 1 follows before half 0 is waited for
+            held = true;
+            continue;
+          }
+          if (held) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            ready();
+            if (lane == 0) mbar_arrive(&sm.q_full[0]);
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          ready();
           if (lane == 0) mbar_arrive(&sm.q_full[hf]);
         }
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");   // left over where a wait ran out
     } else if (!I8 && warp == 9) {
       // --------------------------------------------------------------------------- key tiles, bf16 by TMA
       const int box = a.box_rows, nb = KT / box;   // rows of a box, boxes of a panel of the tile
