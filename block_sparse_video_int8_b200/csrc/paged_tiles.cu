@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
               tmem_ld32(tS + col + c0, xa);
               tmem_wait_ld(xa);
               const int l0 = clo - col - c0, h0 = chi - col - c0;
+              const uint32_t seen = (h0 > 30 ? ~0u : h0 < 0 ? 0u : (2u << h0) - 1u) & (l0 < 1 ? ~0u : l0 > 31 ? 0u : ~0u << l0);
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 float4 f4 = make_float4(a.scale_log2, a.scale_log2, a.scale_log2, a.scale_log2);
@@ -417,9 +418,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
                 const float fs[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  float y = __fmul_rn(__uint_as_float(xa[c + e]), fs[e]);
-                  if (c + e < l0 || c + e > h0) y = -INFINITY;
-                  xa[c + e] = __float_as_uint(y);
+                  const float y = __fmul_rn(__uint_as_float(xa[c + e]), fs[e]);
+                  xa[c + e] = __float_as_uint(seen >> (c + e) & 1u ? y : -INFINITY);
                 }
               }
             };
