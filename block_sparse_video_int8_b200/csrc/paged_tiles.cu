@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         };
         // 64 columns of S at a time become weights over their own place. The quick way takes the running maximum as it
         // is, which holds nearly always: a row whose weights sum to at most kFar has no logit far above it. Where one
-        // does not, the maximum is looked for and the weights are taken again. Tiles that some row does not see whole,
+        // does not, the maximum is looked for and the weights are taken again. Columns that some row does not see whole,
         // and logits past 2^20, go the slow way.
         const float* fkp = sm.fk[ms];
         const int key0 = (it.t0 + j) * KT;
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         for (int sub = 0; sub < 2; ++sub) {
           const int col = 64 * sub;
           float ls = 0.f, es = 0.f;
-          bool quick = whole, done = false, late = sub > 0;   // late: the first half's weights are still to be published
+          bool quick = whole || __all_sync(0xffffffffu, clo <= col && chi >= col + 63), done = false, late = sub > 0;   // late: the first half's weights are still to be published
           auto raise = [&](float mx) {
             if (mx > m + 8.f) {
               const float al = m == -INFINITY ? 0.f : ex2_approx(m - mx);
