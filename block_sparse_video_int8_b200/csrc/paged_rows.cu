@@ -6,7 +6,8 @@
 //
 // The query heads of one key head share its keys: row r of (sequence, key head) is token r / G, head
 // r % G. One CTA = (row tile of 8 * NT rows, split of the keys, key head, sequence); its four warps take
-// 16-key blocks in turn, each with its own running maximum, sum and output, and join at the end.
+// 16-key blocks in turn, each with its own running maximum, sum and output, and join at the end. The splits of a row
+// tile are then joined by their cluster or by a second kernel.
 // Such calls are bound by reading the codes (an INT8 key head's token is 2 d + 8 bytes for 4 d flops a
 // row), and what bounds the reading is how many bytes are on their way: each warp keeps a ring of 16-key
 // blocks of its own in shared memory, filled by cp.async two or three blocks ahead with no registers held
@@ -21,7 +22,7 @@
 // lanes that read together then meet eight different banks, for K and for V.
 // Measured, one token of each sequence, heads of 128 (a copy moves 6.54 TB/s): 64 sequences of 8192 keys, 8 key heads,
 // bf16 pages 323 us (6.66 TB/s), INT8 pages 196 (5.66; issue slots 56 % taken by widening and the softmax, MUFU 5 %);
-// 2 of 131000 keys, 40 key heads, INT8 458 (6.0). The codes through registers instead of the rings took 537 of 458.
+// 2 of 131000 keys, 40 key heads, INT8 458 (6.0; with the codes through registers instead of the rings 537).
 
 #include <climits>
 
