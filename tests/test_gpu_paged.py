@@ -666,3 +666,21 @@ def test_two_graphs_with_one_workspace_in_turn(gpu_lib):
     for z in range(2):
         for g, w in zip(got[z], want[z]):
             assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+# ------------------------------------------------------------- few rows: windows, joins by cluster and by kernel
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,n,G,H", [(1, 1, 5, 1), (3, 2, 7, 1), (4, 1, 2, 6), (1, 1, 1, 2)])
+@pytest.mark.parametrize("causal,window", [(True, 17), (True, 300), (True, 999), (True, 0), (False, 0)])
+def test_few_rows_and_windows(gpu_lib, dtype, d, S, n, G, H, causal, window):
+    # 1 to 9 splits, joined by a cluster (few CTAs) or by the second kernel; sequences much shorter than the longest
+    lens = [(n, 1100), (1, 130), (0, 400), (n, 640)][:S]
+    _attend(Setup(gpu_lib, lens, H, d, 32, dtype, seed=S + G), G * H, causal, window)
+
+
+def test_long_sequences_of_one_head(gpu_lib):
+    # more splits than a cluster joins, up to the second kernel's eight groups a row
+    for n, kv in ((1, 30000), (3, 9000), (130, 20000)):
+        _attend(Setup(gpu_lib, [(n, kv)], 1, 64, 256, torch.int8, seed=n), 2, window=0)
+        _attend(Setup(gpu_lib, [(n, kv)], 1, 64, 256, torch.bfloat16, seed=n), 2, window=kv - 100)
