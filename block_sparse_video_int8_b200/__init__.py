@@ -621,6 +621,7 @@ class KVCache:
 # as they can: one comparison an argument while it is as it should be, messages only when it is not, pointers as plain
 # integers, structs built once.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # the tensors at hand have set CUDA up
 
 
 def _stream_of(stream, index: int) -> int:
@@ -770,7 +771,7 @@ class PagedKVCache:
         """The batch's new tokens, bf16 [T, H, d], into their pages (C ABI ``bsva_paged_kv_write``); tokens may be
         strided, as slices of a fused projection are."""
         index = self._index
-        if torch.cuda.current_device() != index:
+        if _device() != index:
             with torch.cuda.device(index):
                 return self.write(k, v, batch, workspace, stream)
         if stream is not None and workspace is None:
@@ -792,14 +793,14 @@ class PagedKVCache:
         """Cached tokens ``first[s]`` (default 0) to the end of each sequence as bf16 (k, v) [S, H, length, d], zeros
         behind them; ``length`` defaults to ``max_kv`` (C ABI ``bsva_paged_kv_read``)."""
         index = self._index
-        if torch.cuda.current_device() != index:
+        if _device() != index:
             with torch.cuda.device(index):
                 return self.read(batch, first, length, out, workspace, stream)
         if stream is not None and (out is None or workspace is None):
             with _on(stream, index):
                 return self.read(batch, first, length, out, workspace)
-        S = batch.S
-        L = batch.max_kv if length is None else int(length)
+        S = batch._of[0]
+        L = batch._of[2] if length is None else int(length)
         shape = (S, self.H, L, self.d)
         fp = None if first is None else _dense(first, torch.int32, (S,), index, "first")
         if out is None:
@@ -822,7 +823,7 @@ class PagedKVCache:
         ``paged_attn_fwd``). Returns ``out`` [T, Hq, d] or ``(out, lse)``; rows behind the last sequence are left as
         they were (``out`` and ``lse`` that the call allocates: zeros)."""
         index = self._index
-        if torch.cuda.current_device() != index:
+        if _device() != index:
             with torch.cuda.device(index):
                 return self.attend(q, batch, causal, window, softmax_scale, with_lse, workspace, out, lse, stream)
         if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
@@ -875,7 +876,7 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_len: tor
     index = q.get_device()
     if index < 0:
         _need(q, torch.bfloat16, None, "q")
-    if torch.cuda.current_device() != index:
+    if _device() != index:
         with torch.cuda.device(index):
             return cross_attn_fwd(q, k, v, k_len, softmax_scale, with_lse, workspace, out, lse, stream)
     if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
