@@ -684,3 +684,30 @@ def test_long_sequences_of_one_head(gpu_lib):
     for n, kv in ((1, 30000), (3, 9000), (130, 20000)):
         _attend(Setup(gpu_lib, [(n, kv)], 1, 64, 256, torch.int8, seed=n), 2, window=0)
         _attend(Setup(gpu_lib, [(n, kv)], 1, 64, 256, torch.bfloat16, seed=n), 2, window=kv - 100)
+
+
+def test_beside_the_block_sparse_kernel(gpu_lib):
+    # both kernels hold tensor memory; on two streams at once each gives what it gives alone
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Q, K, V = (torch.randn((1, 8, 4096, 64), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    qk = gpu_lib.quantize_qk(Q, K)
+    mask = torch.ones((1, 1, 32, 32), dtype=torch.uint8, device="cuda")
+
+    def sparse():
+        return gpu_lib.masked_block_attn_fwd(qk["q8"], qk["q_scale"], qk["k8"], qk["k_scale"], V, mask)
+    kinds = _call_kinds(gpu_lib, 151)
+    want, want_sparse = [call(workspace=ws) for call, ws in kinds], sparse()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for call, ws in kinds:
+            with torch.cuda.stream(streams[0]):
+                other = sparse()
+            with torch.cuda.stream(streams[1]):
+                got.append(call(workspace=ws))
+        torch.cuda.synchronize()
+        assert torch.equal(other, want_sparse)
+        for (_, ws), x, w in zip(kinds, got, want):
+            gpu_lib.check_status(ws)
+            assert all(torch.equal(a, b) for a, b in zip(x, w))
