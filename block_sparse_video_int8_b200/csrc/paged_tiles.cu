@@ -723,13 +723,16 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           ++no;
         }
         if (lane == 0) {
-          fence_proxy_async_smem();                // the answer before was read
           mbar_arrive_expect_tx(&sm.next_full, 16);
           ask_next_cta(&sm.next_cta, &sm.next_full);
         }
         __syncwarp();
         if (!wait(&sm.next_full, asked++)) break;
         more = next_cta(&sm.next_cta, x, y, z);
+        // every lane has read the answer before the next one may be written over it: a CTA without rows is followed by
+        // the next request at once
+        fence_proxy_async_smem();
+        __syncwarp();
       }
     } else if (I8 ? warp == 9 || warp == 10 : warp == 10) {
       // --------------------------------------------------------------------------------------------- Q

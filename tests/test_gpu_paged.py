@@ -711,3 +711,63 @@ def test_beside_the_block_sparse_kernel(gpu_lib):
         for (_, ws), x, w in zip(kinds, got, want):
             gpu_lib.check_status(ws)
             assert all(torch.equal(a, b) for a, b in zip(x, w))
+
+
+# ------------------------------------------------------ several items with keys a CTA, with and without rows between them
+def _check_heads(st, q, out, lse, heads, causal=True, window=0):
+    G = q.shape[1] // st.H
+    o_, l_ = out.double().cpu().numpy(), None if lse is None else lse.double().cpu().numpy()
+    for s, (n, kv) in enumerate(st.lens):
+        ok = paged.visible(n, kv, causal, window)
+        rows = slice(st.starts[s], st.starts[s] + n)
+        for h in heads:
+            qh, k, v = q[rows, h].double().numpy(), st.values[0][s][:, h // G], st.values[1][s][:, h // G]
+            l = paged.attention_rows(qh, k, v, ok)[1] if l_ is None else l_[rows, h]
+            close(qh, k, v, ok, o_[rows, h], l, None, st.dtype, f"sequence {s} head {h}")
+
+
+@pytest.mark.parametrize("dtype,with_lse", [(torch.int8, True), (torch.bfloat16, True), (torch.bfloat16, False)])
+@pytest.mark.parametrize("d,G,H,window", [(128, 1, 40, 0), (64, 3, 14, 0), (64, 7, 9, 150), (128, 2, 24, 0)])
+def test_many_items_a_cta(gpu_lib, dtype, with_lse, d, G, H, window):
+    # 500 to 700 row tiles on 148 SMs: both halves, one half and no rows follow one another in a CTA, over odd and even
+    # numbers of key tiles, so that every barrier's phase and every ring's stage meets every kind of item
+    lens = [(300, 300), (100, 450), (0, 90), (257, 700), (1, 129), (300, 513), (129, 128 + 129), (40, 40)]
+    st = Setup(gpu_lib, lens, H, d, 64, dtype, seed=G, tail=3)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(G * H)
+    qd, ws = q.cuda(), st.cache.new_workspace(st.batch, G * H, st.T)
+    for _ in range(2):
+        got = st.cache.attend(qd, st.batch, window=window, with_lse=with_lse, workspace=ws)
+        out, lse = got if with_lse else (got, None)
+        gpu_lib.check_status(ws)
+        _check_heads(st, q, out, lse, range(0, G * H, max(1, G * H // 12)), window=window)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+def test_items_between_thousands_without_rows(gpu_lib, dtype):
+    # the bound plans 24 row tiles a sequence and head where one has rows: CTAs ask for the next one many times in a row
+    lens = [(1 + 7 * s % 40, 50 + 31 * s) for s in range(24)]
+    st = Setup(gpu_lib, lens, 4, 64, 16, dtype, seed=161)
+    st.batch = gpu_lib.PagedBatch(st.batch.q_start, st.batch.kv_len, st.batch.page_table, 3000, st.batch.max_kv)
+    for _ in range(2):
+        _attend(st, 8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("with_lse", [True, False])
+def test_cross_attention_many_items_a_cta(gpu_lib, d, with_lse):
+    B, H, Lq, Lk = 2, 40, 1100, 130
+    rng = np.random.default_rng(d)
+    q, k, v = _bf16(rng, (B, H, Lq, d)), _bf16(rng, (B, H, Lk, d)), _bf16(rng, (B, H, Lk, d))
+    lens = [Lk, 100]
+    kl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = gpu_lib.new_cross_attn_workspace(q.cuda(), k.cuda())
+    got = gpu_lib.cross_attn_fwd(q.cuda(), k.cuda(), v.cuda(), k_len=kl, with_lse=with_lse, workspace=ws)
+    gpu_lib.check_status(ws)
+    out, lse = got if with_lse else (got, None)
+    for b, n in enumerate(lens):
+        for h in range(0, H, 5):
+            a = [x[b, h].double().cpu().numpy() for x in (q, k[:, :, :n], v[:, :, :n], out)]
+            ok = np.ones((Lq, n), bool)
+            l = paged.attention_rows(*a[:3], ok)[1] if lse is None else lse[b, h].double().cpu().numpy()
+            close(*a[:3], ok, a[3], l, None, torch.bfloat16, f"batch {b} head {h}")
