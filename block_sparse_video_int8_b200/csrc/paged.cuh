@@ -54,16 +54,17 @@ struct SeqView {
   int n;     // new tokens (query rows a head)
   int kv;    // keys
   int q0;    // first row of the sequence in the packed tensors
+  bool bad;  // a value was outside its range
 };
 
 __device__ __forceinline__ SeqView seq_view(const PagedArgs& a, int s) {
   SeqView r;
-  bool bad = false;
+  r.bad = false;
   if (a.q_start) {
     const int lo = a.q_start[s], hi = a.q_start[s + 1];
     r.q0 = min(max(lo, 0), a.T);
     r.n = min(min(max(hi, r.q0), a.T) - r.q0, a.max_q);
-    bad = r.q0 != lo || r.n != hi - lo;
+    r.bad = r.q0 != lo || r.n != hi - lo;
   } else {
     r.q0 = 0;
     r.n = a.max_q;
@@ -71,11 +72,11 @@ __device__ __forceinline__ SeqView seq_view(const PagedArgs& a, int s) {
   if (a.kv_len) {
     const int kv = a.kv_len[s];
     r.kv = min(max(kv, 0), a.max_kv);
-    bad = bad || kv != r.kv;
+    r.bad = r.bad || kv != r.kv;
   } else {
     r.kv = a.max_kv;
   }
-  if (bad) atomicOr(a.status, kStatusBounds);
+  if (r.bad) atomicOr(a.status, kStatusBounds);
   return r;
 }
 

@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kKvThreads) paged_write_kernel(const PagedArgs
   constexpr int N = 2 * kWriteRows;             // K rows, then V rows
   const int s = blockIdx.z;
   const SeqView sv = seq_view(a, s);
-  if (int(blockIdx.x << shift) >= sv.n) return;
+  // lengths clamped into their bounds give positions of other tokens: nothing is written over those
+  if (sv.bad || int(blockIdx.x << shift) >= sv.n) return;
   const int c = threadIdx.x % LPR;
   uint4 x[N];
   long long dst[kWriteRows];                    // destination row, or -1

@@ -771,3 +771,47 @@ def test_cross_attention_many_items_a_cta(gpu_lib, d, with_lse):
             ok = np.ones((Lq, n), bool)
             l = paged.attention_rows(*a[:3], ok)[1] if lse is None else lse[b, h].double().cpu().numpy()
             close(*a[:3], ok, a[3], l, None, torch.bfloat16, f"batch {b} head {h}")
+
+
+# --------------------------------------------------------------------------- a write that breaks a bound harms no token
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 40])
+def test_write_with_broken_lengths_leaves_the_cache(gpu_lib, dtype, n):
+    # sequence 0 breaks a bound: its tokens are not written anywhere, sequence 1's are where they belong
+    H, kvs = 3, (120, 64)
+    broken = [("kv_len", [kvs[0] + 1, kvs[1]]), ("kv_len", [2 ** 31 - 1, kvs[1]]), ("kv_len", [-3, kvs[1]]),
+              ("q_start", [-1, n, 2 * n]), ("q_start", [2 * n + 1, n, 2 * n])]
+    for name, bad in broken:
+        st = Setup(gpu_lib, [(n, kvs[0]), (n, kvs[1])], H, 64, 16, dtype, seed=n)
+        _write_broken(gpu_lib, st, name, bad, first=1)
+    # sequence 1 has more new tokens than max_q, or than there are rows
+    for ends in ([0, n, 2 * n + 5], [0, n, 2 ** 31 - 1]):
+        st = Setup(gpu_lib, [(n, kvs[0]), (n, kvs[1])], H, 64, 16, dtype, seed=n + 1)
+        _write_broken(gpu_lib, st, "q_start", ends, first=0)
+
+
+def _write_broken(gpu_lib, st, name, bad, first):
+    """Writes with a broken length of the other sequence than ``first``, whose tokens alone are expected in the cache."""
+    def held():
+        return [x.clone().view(torch.uint8) for x in (st.cache.k, st.cache.v, st.cache.k_scale, st.cache.v_scale)
+                if x is not None]
+    ws = st.cache.new_workspace(st.batch, st.H, st.T)
+    before = held()
+    getattr(st.batch, name).copy_(torch.tensor(bad, dtype=torch.int32))
+    st.cache.write(st.new[0], st.new[1], st.batch, workspace=ws)
+    with pytest.raises(gpu_lib.BsvaError) as e:
+        gpu_lib.check_status(ws)
+    assert e.value.code == 6
+    n, kv = st.lens[first]
+    pages = torch.from_numpy(st.table[first][np.arange(kv - n, kv) // st.page].astype(np.int64)).unique()
+    for x, y in zip(before, held()):
+        keep = torch.ones(x.shape[0], dtype=torch.bool)
+        keep[pages] = False
+        assert torch.equal(x[keep.cuda()], y[keep.cuda()]), (name, bad)
+    t = np.arange(kv)
+    pg, off = st.table[first][t // st.page], t % st.page
+    for z, (pool, scale) in enumerate(((st.cache.k, st.cache.k_scale), (st.cache.v, st.cache.v_scale))):
+        got = pool.cpu().float().numpy()[pg, :, off]
+        if st.dtype == torch.int8:
+            got = got.astype(np.float64) * scale.cpu().numpy()[pg, :, off].astype(np.float64)[..., None]
+        assert np.array_equal(got, st.values[z][first]), (name, bad)
