@@ -265,7 +265,11 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         if (a.causal) hi = min(hi, pos);
         if (a.window) lo = max(0, pos - a.window + 1);
       }
-      float m = -INFINITY, l = 0.f, le = 0.f, cn = 1.f;   // l divides O, le is of the unrounded weights
+      // Rows behind the sequence's last one hold what the next sequence's queries or the caller's padding give: they
+      // compute along, but have no vote on how the warp's rows are computed and never raise their maximum.
+      const bool dead = off < 0;
+      auto all = [&](bool x) { return __all_sync(0xffffffffu, dead || x) != 0; };
+      float m = dead ? 0.f : -INFINITY, l = 0.f, le = 0.f, cn = 1.f;   // l divides O, le is of the unrounded weights
       for (int j = 0; j < it.N; ++j) {
         const int ms = (gt + j) % MS;
         alive = wait(&sm.s_full[hf], cnt);
@@ -307,16 +311,16 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         const float* fkp = sm.fk[ms];
         const int key0 = (it.t0 + j) * KT;
         const int clo = max(lo - key0, 0), chi = min(hi - key0, KT - 1);   // columns the row sees
-        const bool whole = __all_sync(0xffffffffu, clo == 0 && chi == KT - 1);
+        const bool whole = all(clo == 0 && chi == KT - 1);
         uint32_t xa[32], xb[32], pk[32];
         bool ahead = false;                      // xa holds the sub-tile's first 32 columns
 #pragma unroll 1
         for (int sub = 0; sub < 2; ++sub) {
           const int col = 64 * sub;
           float ls = 0.f, es = 0.f;
-          bool quick = whole || __all_sync(0xffffffffu, clo <= col && chi >= col + 63), done = false, late = sub > 0;   // late: the first half's weights are still to be published
+          bool quick = whole || all(clo <= col && chi >= col + 63), done = false, late = sub > 0;   // late: the first half's weights are still to be published
           auto raise = [&](float mx) {
-            if (mx > m + 8.f) {
+            if (!dead && mx > m + 8.f) {
               const float al = m == -INFINITY ? 0.f : ex2_approx(m - mx);
               f *= al;
               l *= al;
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
               const float mx = scaled_max(xa, 0, -INFINITY);
               if (m == -INFINITY) m = mx;
             }
-            quick = __all_sync(0xffffffffu, fabsf(m) < 0x1p20f);
+            quick = all(fabsf(m) < 0x1p20f);
           }
           bool looked = false;
 #pragma unroll 1
@@ -388,18 +392,18 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
             es = acc.x + acc.y;
             ls = I8 ? es : ls + ls1;
             tmem_wait_ld(xa);
-            done = looked || __all_sync(0xffffffffu, ls <= kFar);
+            done = looked || all(ls <= kFar);
             if (done) break;
             tmem_ld32(tS + col, xa);
             tmem_wait_ld(xa);
             raise(scaled_max(xa, 0, scaled_max(xb, 32, -INFINITY)));
             looked = true;
-            quick = __all_sync(0xffffffffu, fabsf(m) < 0x1p20f);
+            quick = all(fabsf(m) < 0x1p20f);
           }
           ahead = done;
           if (late) publish(0);
           if ((I8 || looked) && __any_sync(0xffffffffu, f != 1.f) && !(alive = rescale(sub))) break;
-          if (!done && __all_sync(0xffffffffu, clo > col + 63 || chi < col)) {
+          if (!done && all(clo > col + 63 || chi < col)) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) pk[c] = 0;   // no row of the warp sees any of the 64 keys
           } else if (!done) {
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
               weigh(32);
               es = acc.x + acc.y;
               if constexpr (I8) ls = es;
-              if (looked || __all_sync(0xffffffffu, ls <= kFar)) break;
+              if (looked || all(ls <= kFar)) break;
               looked = true;
             }
             if (!alive) break;

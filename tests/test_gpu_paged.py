@@ -815,3 +815,22 @@ def _write_broken(gpu_lib, st, name, bad, first):
         if st.dtype == torch.int8:
             got = got.astype(np.float64) * scale.cpu().numpy()[pg, :, off].astype(np.float64)[..., None]
         assert np.array_equal(got, st.values[z][first]), (name, bad)
+
+
+# ------------------------------------------------------------------------- rows that are not a sequence's do not reach it
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("d,G,n,window", [(64, 2, 75, 0), (128, 1, 141, 0), (128, 1, 141, 60), (64, 3, 75, 0), (64, 5, 1, 0)])
+def test_other_rows_do_not_change_a_sequence(gpu_lib, dtype, d, G, n, window):
+    # the queries of the next sequence and of rows behind the last one share tiles with a sequence's last rows: whatever
+    # they hold, its bits stay
+    st = Setup(gpu_lib, [(n, 300), (max(1, n - 34), 200)], 2, d, 16, dtype, seed=n + G, tail=50)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(2 * G).cuda()
+    want = st.cache.attend(q, st.batch, window=window, with_lse=True)
+    for end in (1, 2):                 # rows before starts[end] keep their queries
+        for fill in (0.0, NAN, 1e30, -1e30, math.inf):
+            x = q.clone()
+            x[st.starts[end]:] = fill
+            got = st.cache.attend(x, st.batch, window=window, with_lse=True)
+            for a, b in zip(got, want):
+                assert torch.equal(a[:st.starts[end]], b[:st.starts[end]]), (end, fill)
