@@ -475,10 +475,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c) = y;
       if (c == 0) a.part_ml[pr] = make_float4(mx, ls, ls, 0.f);
     } else {
-      const float inv = ls > 0.f ? 1.f / ls : 0.f;
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
       *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
           make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-      if (c == 0 && a.lse) a.lse[off / D] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+      if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
     }
   }
   if (!a.cluster) return;
@@ -500,10 +500,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
     const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
                           (long long)(h * a.G + rr % a.G) * a.o_head;
-    const float inv = ls > 0.f ? 1.f / ls : 0.f;
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
     *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
         make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-    if (c == 0 && a.lse) a.lse[off / D] = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+    if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
   }
   cluster_sync();                         // no CTA leaves while another reads its parts
 }
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
     for (int p = g; p < a.nsplit; p += PG) {
       const size_t pr = size_t(p) * a.out_rows + row;
       const float4 ml = a.part_ml[pr];
-      if (ml.x == -INFINITY) continue;   // a split without a key of this row: its output part is not written
+      if (ml.y == 0.f) continue;   // a split without a key of this row: its output part is not written (a NaN goes on)
       const float f = ex2_approx(ml.x - mx);
       const float4 z = *reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c);
       ls += f * ml.y;
@@ -557,10 +557,10 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
     }
   }
   if (!in) return;
-  const float inv = ls > 0.f ? 1.f / ls : 0.f;
+  const float inv = ls == 0.f ? 0.f : 1.f / ls;
   *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
       make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-  if (c == 0 && a.lse) a.lse[row] = le > 0.f ? (mx + log2f(le)) * 0.69314718055994531f : -INFINITY;
+  if (c == 0 && a.lse) a.lse[row] = le == 0.f ? -INFINITY : (mx + log2f(le)) * 0.69314718055994531f;
 }
 
 }  // namespace

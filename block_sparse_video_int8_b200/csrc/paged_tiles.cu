@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         tc_fence_after();
       }
       const float up = I8 && cn != 0.f ? 4096.f / cn : 1.f;
-      const float inv = a.nsplit > 1 ? up : l > 0.f ? up / l : 0.f;
+      const float inv = a.nsplit > 1 ? up : l == 0.f ? 0.f : up / l;   // no keys: zeros; NaN stays NaN
       const size_t pr = size_t(it.sp) * a.out_rows + (off < 0 ? 0 : off / D);
       if (it.N > 0 || a.nsplit == 1) {           // a split without keys leaves its output part unwritten
         // A thread has a row, and rows lie far apart: 64 bytes of each row of the warp at a time go through shared
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
       }
       if (off >= 0) {
         if (a.nsplit > 1) a.part_ml[pr] = make_float4(m, l, LSE ? le : l, 0.f);
-        else if (a.lse) a.lse[off / D] = l > 0.f ? (m + log2f(LSE ? le : l)) * 0.69314718055994531f : -INFINITY;
+        else if (a.lse) a.lse[off / D] = l == 0.f ? -INFINITY : (m + log2f(LSE ? le : l)) * 0.69314718055994531f;
       }
       // the next item's first product writes O: order it after these reads (it waits for this half's weights)
       tc_fence_before();

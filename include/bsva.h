@@ -460,7 +460,9 @@ int bsva_paged_kv_read(const bsva_paged_kv* c, const bsva_paged_batch* b, const 
  *   softmax_scale  <= 0 selects 1/sqrt(d)
  *   out        out: bf16 [T, Hq, d];  lse out, nullable: fp32 [T, Hq] (natural log)
  *   workspace  >= bsva_paged_workspace_bytes(c, b, Hq) bytes, 256-aligned
- * Logits, the softmax and its sums are fp32. The result is the same on every run. */
+ * Logits, the softmax and its sums are fp32. A row whose query or visible keys hold a NaN
+ * gets NaN. The result is the same on every run, and a sequence's does not depend on what
+ * other rows of q hold. */
 int paged_attn_fwd(const bsva_paged_kv* c, const bsva_paged_batch* b, const void* q, long long q_stride,
                    int Hq, int causal, int window, float softmax_scale, void* out, float* lse,
                    void* workspace, size_t workspace_bytes, bsva_stream_t stream);

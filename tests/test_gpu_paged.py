@@ -834,3 +834,56 @@ def test_other_rows_do_not_change_a_sequence(gpu_lib, dtype, d, G, n, window):
             got = st.cache.attend(x, st.batch, window=window, with_lse=True)
             for a, b in zip(got, want):
                 assert torch.equal(a[:st.starts[end]], b[:st.starts[end]]), (end, fill)
+
+
+# --------------------------------------------------------------------------------------------- NaN comes out as NaN
+NAN_LENS = [[(1, 700)] * 3, [(1, 3000)] * 20, [(100, 400), (90, 90)], [(130, 4000)]]
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("lens", NAN_LENS)
+def test_nan_queries_give_nan(gpu_lib, dtype, lens):
+    # a diverged row must not look like one without keys (0 and -inf); the others are what they were, within the bounds
+    st = Setup(gpu_lib, lens, 2, 64, 16, dtype, seed=171)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(4)
+    at = [(0, 1), (st.T // 2, 3), (st.T - 1, 0)]
+    bad = q.clone()
+    for t, h in at:
+        bad[t, h, 5] = NAN
+    out, lse = st.cache.attend(bad.cuda(), st.batch, with_lse=True)
+    for t, h in at:
+        assert torch.isnan(out[t, h]).all() and torch.isnan(lse[t, h])
+    good = st.cache.attend(q.cuda(), st.batch, with_lse=True)
+    for t, h in at:
+        out[t, h], lse[t, h] = good[0][t, h], good[1][t, h]
+    st.check(q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("lens", NAN_LENS)
+def test_nan_keys_give_nan(gpu_lib, dtype, lens):
+    # every row that sees the key
+    st = Setup(gpu_lib, lens, 2, 64, 16, dtype, seed=181)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(4).cuda()
+    for t in (0, min(n for n, _ in lens) // 2 + 20):
+        for h in range(2):
+            pool = st.cache.k_scale if dtype == torch.int8 else st.cache.k
+            row = pool[st.table[0][t // 16], h, t % 16]
+            keep = row.clone()
+            row.fill_(NAN)
+            out, lse = st.cache.attend(q, st.batch, with_lse=True)
+            row.copy_(keep)
+            n, kv = lens[0]
+            rows = slice(max(0, t - (kv - n)), n)
+            assert torch.isnan(out[rows, 2 * h:2 * h + 2]).all() and torch.isnan(lse[rows, 2 * h:2 * h + 2]).all()
+
+
+def test_nan_queries_in_cross_attention(gpu_lib):
+    for Lq in (3, 200):
+        q, k, v = (torch.ones((1, 2, L, 64), dtype=torch.bfloat16, device="cuda") for L in (Lq, 300, 300))
+        q[0, 1, Lq - 1, 0] = NAN
+        out, lse = gpu_lib.cross_attn_fwd(q, k, v, with_lse=True)
+        assert torch.isnan(out[0, 1, Lq - 1]).all() and torch.isnan(lse[0, 1, Lq - 1])
+        assert (out[0, 0] == 1).all() and (out[0, 1, :Lq - 1] == 1).all()
