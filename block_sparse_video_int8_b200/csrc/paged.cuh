@@ -22,9 +22,9 @@ struct PagedArgs {
   const __nv_bfloat16* q;       // element strides below
   __nv_bfloat16* out;
   float* lse;                   // [out rows], nullable
-  float* part_o;                // [nsplit, out rows, d] unnormalised partial outputs
+  float* part_o;                // [nsplit, out rows, d] outputs of the splits, each divided by its sum
   float4* part_ml;              // [nsplit, out rows] (running max in log2 units, sum that divides O, sum of the
-                                // unrounded weights, unused)
+                                // unrounded weights, unused); sums times kDown
   uint32_t* status;
   long long q_seq, q_tok, q_head;   // q strides (q_seq: contiguous source only)
   long long o_seq, o_tok, o_head;   // out strides; out row index = offset / d
@@ -123,6 +123,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// Sums of weights are kept times 2^-48, those of bf16 values as sums of weights times 2^-48, and outputs are divided by
+// their sum before they are joined: the sums of 2^30 keys' weights stay below one, and so every weighted sum of values
+// below the largest of them, whatever its size. (The price: a weighted value below 2^-126 loses bits, so values below 2^-54
+// have less than fp32's precision, and weights below 2^-78 of the largest are lost.)
+constexpr float kDown = 0x1p-48f, kUp = 0x1p48f, kDownLog2 = 48.f;
 
 // ---- INT8 values in an f16 product: the scale s_v of a key's values enters as s_v * c with c a power of two, so
 // that it fits f16 whatever the scales' range: c = 1 / 2^floor(log2 s), s the largest scale seen when c was set, and

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       for (int e = 0; e < 4; ++e) {
         const float mu = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
         p[e] = ex2_approx(x[nt][e] - mu);
+        if constexpr (!I8) p[e] *= kDown;
         l[nt][e & 1] += p[e];
       }
       if constexpr (I8) {
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 
-  // ---- join the four warps: each leaves its maximum, sum and output (over cn) in shared memory
+  // ---- join the four warps: each leaves its maximum, sum and output (over the sum and cn) in shared memory
   constexpr int W = kRowThreads / 32, NR = 8 * NT;
   __shared__ float s_m[W][NR], s_l[W][NR];
   __shared__ float2 s_ml[NR];             // of the CTA, for its cluster
@@ -435,17 +436,18 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
       const int r = 8 * nt + 2 * t + e;
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
       if (g == 0) {
         s_m[warp][r] = m[nt][e];
-        s_l[warp][r] = ls;
+        s_l[warp][r] = I8 ? ls * kDown : ls;
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
         // lane's d values: of each of its pieces, 16 bytes of codes or values, 8 for INT8 rows of 64
         constexpr int PV = VB < 16 ? VB : 16 / EB;
         const int d0 = (2 * j / PV) * 8 * PV + g * PV + 2 * j % PV;
-        s_o[warp][r][d0] = o[nt][j][e] * inv_c;
-        s_o[warp][r][d0 + 1] = o[nt][j][e + 2] * inv_c;
+        s_o[warp][r][d0] = o[nt][j][e] * inv * inv_c;
+        s_o[warp][r][d0 + 1] = o[nt][j][e + 2] * inv * inv_c;
       }
     }
   __syncthreads();
@@ -460,13 +462,15 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float f = s_m[w][r] == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - mx);
+      const float f = (s_m[w][r] == -INFINITY ? 0.f : ex2_approx(s_m[w][r] - mx)) * s_l[w][r];
       const float4 z = *reinterpret_cast<const float4*>(&s_o[w][r][4 * c]);
-      ls += f * s_l[w][r];
+      ls += f;
       y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
     }
     const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
                           (long long)(h * a.G + rr % a.G) * a.o_head;
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
     if (a.cluster) {
       *reinterpret_cast<float4*>(&s_o[0][r][4 * c]) = y;
       if (c == 0) s_ml[r] = make_float2(mx, ls);
@@ -475,10 +479,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
       *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c) = y;
       if (c == 0) a.part_ml[pr] = make_float4(mx, ls, ls, 0.f);
     } else {
-      const float inv = ls == 0.f ? 0.f : 1.f / ls;
-      *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
-          make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-      if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
+      *reinterpret_cast<uint2*>(a.out + off + 4 * c) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls * kUp)) * 0.69314718055994531f;
     }
   }
   if (!a.cluster) return;
@@ -494,8 +496,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     for (int p = 0; p < a.nsplit; ++p) {
       const float2 ml = ld_cluster2(in_cta(&s_ml[r], p));
       const float4 z = ld_cluster4(in_cta(&s_o[0][r][4 * c], p));
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-      ls += f * ml.y;
+      const float f = (ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx)) * ml.y;
+      ls += f;
       y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
     }
     const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     const float inv = ls == 0.f ? 0.f : 1.f / ls;
     *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
         make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-    if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * 0.69314718055994531f;
+    if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls * kUp)) * 0.69314718055994531f;
   }
   cluster_sync();                         // no CTA leaves while another reads its parts
 }
@@ -530,10 +532,10 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
       const size_t pr = size_t(p) * a.out_rows + row;
       const float4 ml = a.part_ml[pr];
       if (ml.y == 0.f) continue;   // a split without a key of this row: its output part is not written (a NaN goes on)
-      const float f = ex2_approx(ml.x - mx);
+      const float e = ex2_approx(ml.x - mx), f = e * ml.y;
       const float4 z = *reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c);
-      ls += f * ml.y;
-      le += f * ml.z;
+      ls += f;
+      le += e * ml.z;
       y.x += f * z.x; y.y += f * z.y; y.z += f * z.z; y.w += f * z.w;
     }
   }
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
   const float inv = ls == 0.f ? 0.f : 1.f / ls;
   *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
       make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
-  if (c == 0 && a.lse) a.lse[row] = le == 0.f ? -INFINITY : (mx + log2f(le)) * 0.69314718055994531f;
+  if (c == 0 && a.lse) a.lse[row] = le == 0.f ? -INFINITY : (mx + log2f(le * kUp)) * 0.69314718055994531f;
 }
 
 }  // namespace

@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
     const uint32_t tS = tmem + lanes + S_COL + hf * KT, tO = tmem + lanes + O_COL + hf * D;
     // how far a row's weights may sum before its maximum is raised: f16 holds 2^15 (and a maximum that was looked
     // for leaves 64 weights of 2^8 at most), bf16 the range of fp32
-    constexpr float kFar = I8 ? 0x1p15f : 0x1p40f;
+    // (there all weights are times kDown: 2^24 sub-tiles of 2^24 each sum to at most one)
+    constexpr float kFar = I8 ? 0x1p15f : 0x1p24f * kDown;
     Item it;
     uint32_t gt = 0, cnt = 0;                    // key tiles, key tiles of this half
     bool alive = true;
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           bool looked = false;
 #pragma unroll 1
           while (quick) {
-            const float2 nm = make_float2(-m, -m), sc = make_float2(a.scale_log2, a.scale_log2);
+            const float mu = I8 ? m : m + kDownLog2;
+            const float2 nm = make_float2(-mu, -mu), sc = make_float2(a.scale_log2, a.scale_log2);
             float2 acc = make_float2(0.f, 0.f);
             float ls1 = 0.f;
             ls = 0.f;
@@ -450,8 +452,10 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
                 masked(c0);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                  const float2 p = make_float2(ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c]), -mu)),
-                                               ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c + 1]), -mu)));
+                  float2 p = make_float2(ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c]), -mu)),
+                                         ex2_approx(__fadd_rn(__uint_as_float(xa[2 * c + 1]), -mu)));
+                  // (a maximum of any size: 48 added to it could be rounded away)
+                  if constexpr (!I8) p = make_float2(p.x * kDown, p.y * kDown);
                   acc = __fadd2_rn(acc, p);
                   pk[c0 / 2 + c] = I8 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
                   if constexpr (!I8) add_bf16x2(ls, pk[c0 / 2 + c]);
@@ -480,8 +484,9 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         if (!(alive = wait(&sm.pv_done[hf][1], cnt - 1))) break;
         tc_fence_after();
       }
-      const float up = I8 && cn != 0.f ? 4096.f / cn : 1.f;
-      const float inv = a.nsplit > 1 ? up : l == 0.f ? 0.f : up / l;   // no keys: zeros; NaN stays NaN
+      // O over its sum and, INT8, over c / 4096: in two steps, since 4096 / c alone may be past the largest float
+      const float inv = (l == 0.f ? 0.f : 1.f / l) * (I8 ? 4096.f : 1.f);   // no keys: zeros; NaN stays NaN
+      const float up = I8 && cn != 0.f ? 1.f / cn : 1.f;
       const size_t pr = size_t(it.sp) * a.out_rows + (off < 0 ? 0 : off / D);
       if (it.N > 0 || a.nsplit == 1) {           // a split without keys leaves its output part unwritten
         // A thread has a row, and rows lie far apart: 64 bytes of each row of the warp at a time go through shared
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           float y[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c)           // INT8: columns 4g + 1 and 4g + 2 stand for each other's d value
-            y[c] = __uint_as_float(o[I8 ? (c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1) : c]) * inv;
+            y[c] = __uint_as_float(o[I8 ? (c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1) : c]) * inv * up;
           uint4 w[4];
           if (a.nsplit > 1) {
 #pragma unroll
@@ -541,8 +546,9 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         }
       }
       if (off >= 0) {
-        if (a.nsplit > 1) a.part_ml[pr] = make_float4(m, l, LSE ? le : l, 0.f);
-        else if (a.lse) a.lse[off / D] = l == 0.f ? -INFINITY : (m + log2f(LSE ? le : l)) * 0.69314718055994531f;
+        const float down = I8 ? kDown : 1.f;
+        if (a.nsplit > 1) a.part_ml[pr] = make_float4(m, l * down, (LSE ? le : l) * down, 0.f);
+        else if (a.lse) a.lse[off / D] = l == 0.f ? -INFINITY : (m + log2f((LSE ? le : l) * down * kUp)) * 0.69314718055994531f;
       }
       // the next item's first product writes O: order it after these reads (it waits for this half's weights)
       tc_fence_before();

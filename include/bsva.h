@@ -385,7 +385,9 @@ int masked_block_attn_fwd_kvcache(const bsva_kv_cache* c, int Lq, const int8_t* 
  * BSVA_KV_INT8 holds codes with one scale per (token, head): s = fl32(amax/127) over
  * the d values, code = rint_half_even(fl32(x/s)), 0 where s = 0; the cached value is
  * code * s. BSVA_KV_BF16 holds the values themselves. Values must be finite: a key that
- * holds an infinity or a NaN can spoil rows of its sequence that do not see it.
+ * holds an infinity or a NaN can spoil rows of its sequence that do not see it. Finite
+ * ones may be as large as the type holds; attention to values whose magnitudes are below
+ * 2^-54 keeps fewer bits of them.
  * The caller allocates the buffers (not necessarily initialised: a row is read only
  * once it has been written). */
 enum bsva_kv_dtype {

@@ -887,3 +887,51 @@ def test_nan_queries_in_cross_attention(gpu_lib):
         out, lse = gpu_lib.cross_attn_fwd(q, k, v, with_lse=True)
         assert torch.isnan(out[0, 1, Lq - 1]).all() and torch.isnan(lse[0, 1, Lq - 1])
         assert (out[0, 0] == 1).all() and (out[0, 1, :Lq - 1] == 1).all()
+
+
+# ------------------------------------------------------------------------------- values up to the largest finite ones
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[(1, 700)] * 3, [(1, 3000)] * 20, [(1, 9)], [(100, 400), (90, 90)], [(130, 4000)]])
+def test_the_largest_values(gpu_lib, dtype, d, lens):
+    # values of 2^126 to 2^127: a weighted mean is finite, a sum of two is not; all of one sign, so that no error hides
+    st = Setup(gpu_lib, lens, 2, d, 16, dtype, seed=191)
+    for s, (n, kv) in enumerate(lens):
+        x = (1 + torch.rand((kv, 2, d), generator=torch.Generator().manual_seed(s))).mul(2.0 ** 126).to(torch.bfloat16)
+        codes, sc = paged.quantize_rows(x.float().numpy())
+        st.values[1][s] = paged.dequantize_rows(codes, sc) if dtype == torch.int8 else x.double().numpy()
+        t = np.arange(kv)
+        pg = torch.from_numpy(st.table[s][t // 16].astype(np.int64)).cuda()
+        off = torch.from_numpy(t % 16).cuda()
+        if dtype == torch.int8:
+            st.cache.v[pg, :, off] = torch.from_numpy(codes).cuda()
+            st.cache.v_scale[pg, :, off] = torch.from_numpy(sc).cuda()
+        else:
+            st.cache.v[pg, :, off] = x.cuda()
+        if n:
+            st.new[1][st.starts[s]:st.starts[s + 1]] = x[kv - n:].cuda()
+    _attend(st, 4)
+    _attend(st, 4, qscale=20.0)
+
+
+@pytest.mark.parametrize("Lq", [1, 300])
+def test_the_largest_values_in_cross_attention(gpu_lib, Lq):
+    g = torch.Generator().manual_seed(Lq)
+    q, k = (torch.randn((2, 2, L, 64), generator=g).to(torch.bfloat16) for L in (Lq, 500))
+    v = (1 + torch.rand((2, 2, 500, 64), generator=g)).mul(2.0 ** 126).to(torch.bfloat16)
+    out, lse = gpu_lib.cross_attn_fwd(q.cuda(), k.cuda(), v.cuda(), with_lse=True)
+    for b in range(2):
+        for h in range(2):
+            close(*[x[b, h].double().numpy() for x in (q, k, v)], np.ones((Lq, 500), bool), out[b, h].double().cpu().numpy(),
+                  lse[b, h].double().cpu().numpy(), None, torch.bfloat16, f"batch {b} head {h}")
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[(1, 700)] * 3, [(1, 3000)] * 20, [(100, 400), (90, 90)], [(130, 4000)]])
+def test_values_of_small_magnitude(gpu_lib, dtype, lens):
+    # all values times 2^-50 (exact): outputs are what they are at ordinary magnitudes, times 2^-50, within the bounds
+    st = Setup(gpu_lib, lens, 2, 64, 16, dtype, seed=201, mag=0.3)
+    (st.cache.v_scale if dtype == torch.int8 else st.cache.v).mul_(2.0 ** -50)
+    st.new[1].mul_(2.0 ** -50)
+    st.values[1] = [x * 2.0 ** -50 for x in st.values[1]]
+    _attend(st, 4)
