@@ -935,3 +935,17 @@ def test_values_of_small_magnitude(gpu_lib, dtype, lens):
     st.new[1].mul_(2.0 ** -50)
     st.values[1] = [x * 2.0 ** -50 for x in st.values[1]]
     _attend(st, 4)
+
+
+def test_the_largest_values_under_weights_above_the_first_maximum(gpu_lib):
+    # the first keys' logits are 33 powers of two below all others': their maximum is kept, each later key weighs 2^33, and
+    # their sum over one long pass (as many row tiles as SMs: no splits) must not reach the top of fp32
+    Lq, Lk, d = 256 * 148, 50000, 64
+    q, k, v = (torch.zeros((1, 1, L, d), dtype=torch.bfloat16, device="cuda") for L in (Lq, Lk, Lk))
+    q[..., 0], k[0, 0, 64:, 0] = 1.0, 22.75
+    v[:] = (1 + torch.rand((Lk, 1), generator=torch.Generator().manual_seed(1))).mul(2.0 ** 126).to(torch.bfloat16).cuda()
+    out, lse = gpu_lib.cross_attn_fwd(q, k, v, softmax_scale=1.0, with_lse=True)
+    assert (out == out[:, :, :1]).all() and (lse == lse[:, :, :1]).all()
+    close(*[x[0, 0, :1].double().cpu().numpy() if x is q else x[0, 0].double().cpu().numpy() for x in (q, k, v)],
+          np.ones((1, Lk), bool), out[0, 0, :1].double().cpu().numpy(), lse[0, 0, :1].double().cpu().numpy(), 1.0,
+          torch.bfloat16, "first row")
