@@ -118,6 +118,9 @@ __device__ __forceinline__ void widen_f16(uint32_t w, uint32_t& even, uint32_t& 
   odd = half(w >> 8);
 }
 
+// 1 / sum, 0 for the sum of no weights. Within 2 units of the last place, for sums in [2^-126, 2^126].
+__device__ __forceinline__ float over_sum(float x) { return x == 0.f ? 0.f : __fdividef(1.f, x); }
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

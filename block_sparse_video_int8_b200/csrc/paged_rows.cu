@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
       const int r = 8 * nt + 2 * t + e;
-      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      const float inv = over_sum(ls);
       if (g == 0) {
         s_m[warp][r] = m[nt][e];
         s_l[warp][r] = I8 ? ls * kDown : ls;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
     const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
                           (long long)(h * a.G + rr % a.G) * a.o_head;
-    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    const float inv = over_sum(ls);
     y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
     if (a.cluster) {
       *reinterpret_cast<float4*>(&s_o[0][r][4 * c]) = y;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
     const long long off = (long long)s * a.o_seq + (long long)(sv.q0 + rr / a.G) * a.o_tok +
                           (long long)(h * a.G + rr % a.G) * a.o_head;
-    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    const float inv = over_sum(ls);
     *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
         make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
     if (c == 0 && a.lse) a.lse[off / D] = ls == 0.f ? -INFINITY : (mx + log2f(ls * kUp)) * 0.69314718055994531f;
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a) {
     }
   }
   if (!in) return;
-  const float inv = ls == 0.f ? 0.f : 1.f / ls;
+  const float inv = over_sum(ls);
   *reinterpret_cast<uint2*>(a.out + off + 4 * c) =
       make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
   if (c == 0 && a.lse) a.lse[row] = le == 0.f ? -INFINITY : (mx + log2f(le * kUp)) * 0.69314718055994531f;

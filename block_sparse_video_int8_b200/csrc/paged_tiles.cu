@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         tc_fence_after();
       }
       // O over its sum and, INT8, over c / 4096: in two steps, since 4096 / c alone may be past the largest float
-      const float inv = (l == 0.f ? 0.f : 1.f / l) * (I8 ? 4096.f : 1.f);   // no keys: zeros; NaN stays NaN
+      const float inv = over_sum(l) * (I8 ? 4096.f : 1.f);   // no keys: zeros; NaN stays NaN
       const float up = I8 && cn != 0.f ? 1.f / cn : 1.f;
       const size_t pr = size_t(it.sp) * a.out_rows + (off < 0 ? 0 : off / D);
       if (it.N > 0 || a.nsplit == 1) {           // a split without keys leaves its output part unwritten
