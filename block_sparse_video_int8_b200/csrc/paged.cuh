@@ -133,16 +133,20 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // have less than fp32's precision, and weights below 2^-78 of the largest are lost.)
 constexpr float kDown = 0x1p-48f, kUp = 0x1p48f, kDownLog2 = 48.f;
 
-// ---- INT8 values in an f16 product: the scale s_v of a key's values enters as s_v * c with c a power of two, so
-// that it fits f16 whatever the scales' range: c = 1 / 2^floor(log2 s), s the largest scale seen when c was set, and
-// s_v * c < 2^3 by kScaleGrow. Few rows: the weight is p * s_v * c < 2^11, p <= 2^8 by the lazy running maximum.
-// Tiles: the value is code * s_v * c / 4096 < 2^-2. f16 keeps 11 bits of either where bf16 would keep 8; the sum of
-// the weights takes p itself, in fp32. Scales far below the largest one reach f16's subnormals: a key's weighted
-// values are off by 2^-20 of the largest value at most.
-constexpr float kScaleGrow = 8.f;    // s_v * c reaches this: c is set anew and the output so far rescaled
-__device__ __forceinline__ float scale_norm(float s) {   // 2^-floor(log2 s), both in the normal range
-  const int e = min(max(int(__float_as_uint(s) >> 23), 1), 253);
-  return __uint_as_float(uint32_t(254 - e) << 23);
+// ---- INT8 values in an f16 product: the scale s_v of a key's values enters as s_v * c with c a power of two, so that it
+// fits f16 whatever the scales' range. c is set by the largest scale S of the keys met so far that some row of the tile
+// sees, and set anew (the output so far rescaled) when a scale comes that would leave f16; it never falls.
+// Few rows: the weight is p * s_v * c, p <= 2^8 by the lazy running maximum, 2^6 <= S c < 2^7. Tiles: the value is
+// code * (s_v * c), 2^5 <= S c < 2^8. Both are rounded within 2^-11 (tiles: the product and its factor), as far as they
+// are normal in f16, 2^-14: that is so for keys with s_v >= 2^-19 S (few rows, those that weigh at least 1: 2^-20 S),
+// and below each halving costs a bit of what such a key adds. The sum of the weights takes p itself, in fp32.
+constexpr int kRowsUp = 6, kTilesUp = 5;                       // log2 of S c when c is set, rounded down
+constexpr float kRowsFull = 128.f, kTilesFull = 256.f;         // s_v * c reaches this: c is set anew
+// 2^UP * 2^-floor(log2 s), it and its reciprocal in the normal range
+template <int UP>
+__device__ __forceinline__ float scale_norm(float s) {
+  const int e = min(max(int(__float_as_uint(s) >> 23), UP + 1), 253);
+  return __uint_as_float(uint32_t(254 + UP - e) << 23);
 }
 
 cudaError_t launch_paged_write(const PagedArgs& a, bool int8, const __nv_bfloat16* k, const __nv_bfloat16* v,

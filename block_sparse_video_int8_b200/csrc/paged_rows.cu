@@ -339,9 +339,9 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     float c0 = 1.f, c1 = 1.f;             // INT8: weight of a key's codes, s_v * cn
     if constexpr (I8) {
       const float mine = fmaxf(vs[0], vs[1]);
-      if (__any_sync(0xffffffffu, mine * cn >= kScaleGrow || (cn == 0.f && mine > 0.f))) {
+      if (__any_sync(0xffffffffu, mine * cn >= kRowsFull || (cn == 0.f && mine > 0.f))) {
         const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
-        const float c = scale_norm(top), f = cn == 0.f ? 1.f : c / cn;
+        const float c = scale_norm<kRowsUp>(top), f = cn == 0.f ? 1.f : c / cn;
         cn = c;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

@@ -20,7 +20,7 @@
 //                   cp.async otherwise.
 //   warp 11         finds the next item.
 // The scales of INT8 keys enter in the softmax, x = S * (s_k scale log2 e), a vector of 128 a tile; those of the
-// values in their f16 widening, v8 * (s_v c) 2^-12 with the power of two c (paged.cuh), which costs a value a rounding of
+// values in their f16 widening, v8 * (s_v c) with the power of two c (paged.cuh), which costs a value two roundings of
 // 2^-11 at most, as the f16 weight has one. (Both scales as vectors of the softmax took 4000 cycles a half and tile
 // where one takes 2600.)
 // Widened words hold four codes as pairs (0, 2), (1, 3): K's bytes are put in order first; V's columns, and so
@@ -50,7 +50,8 @@ constexpr uint32_t kTileTmem = 512;
 struct Item {
   int s, h, sp, rb;                     // sequence, key head, split, first row
   int R, kv, past, q0;                  // rows of (sequence, key head), keys, keys before the chunk, first token row
-  int lo_all, t0, N;                    // first key that some row sees; first key tile, key tiles
+  int lo_all, hi_all;                   // first key that some row sees, one past the last
+  int t0, N;                            // first key tile, key tiles
   int nh;                               // row halves in use; 0 = no more items
 };
 
@@ -113,10 +114,9 @@ __device__ __forceinline__ bool next_cta(const uint4* answer, int& x, int& y, in
   return got != 0;
 }
 
-// Widening with one multiply-add a pair: a code b xor 0x80 = b + 128 in the low byte of a 16-bit float is the subnormal
-// (b + 128) 2^-133 (bf16) or 2^-24 (f16), which both the multiply-add and its exact product take as it is. Words hold
-// four codes b0 .. b3, the results the pairs (b0, b2) and (b1, b3).
-// bf16: (b + 128) 2^-133 * 2^127 - 2 = b / 64, exact.
+// Words hold four codes b0 .. b3, the results the pairs (b0, b2) and (b1, b3).
+// bf16, with one multiply-add a pair: a code b xor 0x80 = b + 128 in the low byte of a bf16 is the subnormal
+// (b + 128) 2^-133, which both the multiply-add and its exact product take as it is: times 2^127, - 2 = b / 64, exact.
 __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& even, uint32_t& odd) {
   auto pair = [](uint32_t x) {
     uint32_t u = lop_and_xor(x, 0x00ff00ffu, 0x00800080u), r;
@@ -126,18 +126,12 @@ __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& even, uint32_t&
   even = pair(w);
   odd = pair(w >> 8);
 }
-// f16 times f (a pair of equal f16): (b + 128) 2^-24 * f - 2^-17 f = b (2^-24 f), rounded once; 2^-17 f is exact, or
-// off by at most 2^-25 where it is subnormal, as the result then is.
+// f16 times f (a pair of equal f16): the codes exactly (paged.cuh), then one rounding. (The subnormals above would do it
+// in one multiply-add, but only up to 2^-1, where values 2^10 below the largest are subnormal themselves.)
 __device__ __forceinline__ void values_f16(uint32_t w, uint32_t f, uint32_t& even, uint32_t& odd) {
-  uint32_t c;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(f), "r"(0x80808080u));   // two of -2^-17
-  auto pair = [&](uint32_t x) {
-    uint32_t u = lop_and_xor(x, 0x00ff00ffu, 0x00800080u), r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(u), "r"(f), "r"(c));
-    return r;
-  };
-  even = pair(w);
-  odd = pair(w >> 8);
+  widen_f16(w, even, odd);
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(even) : "r"(f));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(odd) : "r"(f));
 }
 
 // sum += both halves of a pair of bf16
@@ -487,8 +481,8 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         if (!(alive = wait(&sm.pv_done[hf][1], cnt - 1))) break;
         tc_fence_after();
       }
-      // O over its sum and, INT8, over c / 4096: in two steps, since 4096 / c alone may be past the largest float
-      const float inv = over_sum(l) * (I8 ? 4096.f : 1.f);   // no keys: zeros; NaN stays NaN
+      // O over its sum and, INT8, over c: in two steps, since 1 / (l c) may leave the range of floats
+      const float inv = over_sum(l);             // no keys: zeros; NaN stays NaN
       const float up = I8 && cn != 0.f ? 1.f / cn : 1.f;
       const size_t pr = size_t(it.sp) * a.out_rows + (off < 0 ? 0 : off / D);
       if (it.N > 0 || a.nsplit == 1) {           // a split without keys leaves its output part unwritten
@@ -588,7 +582,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
         // The page table is read once a key, two tiles ahead of the keys, and looked at a tile later: a look at once
         // would wait for it. -1: no key.
         auto key_of = [&](int j) { return (it.t0 + j) * KT + lt; };
-        auto live = [&](int j) { return j < it.N && key_of(j) >= it.lo_all && key_of(j) < it.kv; };
+        auto live = [&](int j) { return j < it.N && key_of(j) >= it.lo_all && key_of(j) < it.hi_all; };
         auto entry = [&](int j) { return live(j) ? page_entry(a, it.s, key_of(j)) : 0; };
         auto row_of = [&](int j, int e) -> int {   // fits: 2^31 rows would be 275 GB of codes
           return live(j) ? int(kv_row(a, checked_page(a, e), it.h, key_of(j))) : -1;
@@ -636,13 +630,13 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           if (!(ok = wait(&sm.r_full, turn++))) break;
           const float top = __uint_as_float(max(max(sm.red[st][0], sm.red[st][1]), max(sm.red[st][2], sm.red[st][3])));
           float rs = 1.f;
-          if (top * cn >= kScaleGrow || (cn == 0.f && top > 0.f)) {
-            const float n = scale_norm(top);
+          if (top * cn >= kTilesFull || (cn == 0.f && top > 0.f)) {
+            const float n = scale_norm<kTilesUp>(top);
             if (cn != 0.f) rs = n / cn;
             cn = n;
           }
           sm.fk[ms][lt] = sk * (64.f * a.scale_log2);                           // K enters as code / 64
-          sm.sv[st][lt] = pack_f16x2(svv * cn * 4096.f, svv * cn * 4096.f);     // times 2^-24: V as code * s_v c / 4096
+          sm.sv[st][lt] = pack_f16x2(svv * cn, svv * cn);
           if (lt == 0) {
             sm.rs[ms] = rs;
             sm.cn[ms] = cn;
@@ -709,11 +703,11 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
           const int rows = min(256, it.R - it.rb);
           if (rows > 0) {
             it.nh = rows > 128 ? 2 : 1;
-            const int hi = a.causal ? min(sv.kv, it.past + (it.rb + rows - 1) / a.G + 1) : sv.kv;
+            it.hi_all = a.causal ? min(sv.kv, it.past + (it.rb + rows - 1) / a.G + 1) : sv.kv;
             it.lo_all = a.window ? max(0, it.past + it.rb / a.G - a.window + 1) : 0;
             it.t0 = it.lo_all / KT;
-            if (hi > it.lo_all) {
-              it.N = (hi + KT - 1) / KT - it.t0;
+            if (it.hi_all > it.lo_all) {
+              it.N = (it.hi_all + KT - 1) / KT - it.t0;
               if (a.nsplit > 1) {
                 const int per = (it.N + a.nsplit - 1) / a.nsplit;
                 it.t0 += it.sp * per;

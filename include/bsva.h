@@ -387,7 +387,10 @@ int masked_block_attn_fwd_kvcache(const bsva_kv_cache* c, int Lq, const int8_t* 
  * code * s. BSVA_KV_BF16 holds the values themselves. Values must be finite: a key that
  * holds an infinity or a NaN can spoil rows of its sequence that do not see it. Finite
  * ones may be as large as the type holds; attention to values whose magnitudes are below
- * 2^-54 keeps fewer bits of them.
+ * 2^-54 keeps fewer bits of them. INT8 values enter the second product as f16 relative to
+ * the largest value scale among the keys that a tile of query rows sees (16 rows or, in
+ * chunks, 256): keys with scales down to 2^-19 of it keep their precision, below that each
+ * halving costs them a bit.
  * The caller allocates the buffers (not necessarily initialised: a row is read only
  * once it has been written). */
 enum bsva_kv_dtype {

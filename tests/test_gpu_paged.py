@@ -949,3 +949,59 @@ def test_the_largest_values_under_weights_above_the_first_maximum(gpu_lib):
     close(*[x[0, 0, :1].double().cpu().numpy() if x is q else x[0, 0].double().cpu().numpy() for x in (q, k, v)],
           np.ones((1, Lk), bool), out[0, 0, :1].double().cpu().numpy(), lse[0, 0, :1].double().cpu().numpy(), 1.0,
           torch.bfloat16, "first row")
+
+
+# -------------------------------------------------------------- one token whose values are far larger than the others'
+@pytest.mark.parametrize("lens,page,window,big", [
+    ([(200, 200)], 16, 0, 199),          # tiles: only the last row sees it, those before share its tile of rows and keys
+    ([(200, 460)], 64, 0, 455),
+    ([(130, 300)], 16, 90, 82),          # at the first rows' end of the window: gone for the later ones
+    ([(10, 300)], 16, 0, 299),           # few rows
+    ([(10, 10)], 16, 0, 9),
+    ([(10, 300)], 16, 40, 252),
+    ([(1, 300)], 16, 0, 150)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [8, 12, 16])
+def test_small_values_beside_a_large_one(gpu_lib, lens, page, window, big, d, power):
+    """INT8. A row's bound has only what it sees in it, but for the steps of f16 below 2^-14, which are relative to the
+    largest scale S that its tile of rows meets: R = S / s for a visible scale s.
+
+    Tiles: a value enters as code * f, f = s c with 2^5 <= S c < 2^8, so f >= 2^5 / R >= 2^-14 for R <= 2^19: f and the
+    product round within 2^-11 each, but for products below 2^-14 that lose 2^-25, 2^-25 / c <= 2^-30 S of a value.
+    A weight rounds within 2^-11, or by 2^-25 below 2^-14 (n 2^-25 max|v| over the visible keys; relative to a largest
+    weight of at least 1).
+    Few rows: a weight enters as p s c with 2^6 <= S c < 2^7, rounded within 2^-11, or below 2^-14 by at most 2^-25 and
+    never by more than itself: of p s that is min(2^-31 S, p s), times codes of at most 127."""
+    (n, kv), H, G = lens[0], 1, 2
+    st = Setup(gpu_lib, lens, H, d, page, torch.int8, seed=power, mag=0.3)
+    x = st.kv[1][0]
+    x[big] *= 2.0 ** power
+    codes, sc = paged.quantize_rows(x.float().numpy())
+    st.values[1][0] = paged.dequantize_rows(codes, sc)
+    t = np.arange(kv)
+    pg, off = torch.from_numpy(st.table[0][t // page].astype(np.int64)).cuda(), torch.from_numpy(t % page).cuda()
+    st.cache.v[pg, :, off] = torch.from_numpy(codes).cuda()
+    st.cache.v_scale[pg, :, off] = torch.from_numpy(sc).cuda()
+    st.cache.write(st.new[0], x[kv - n:].cuda(), st.batch)
+    q = st.queries(G)
+    ws = st.cache.new_workspace(st.batch, G, st.T)
+    out, _ = st.cache.attend(q.cuda(), st.batch, window=window, with_lse=True, workspace=ws)
+    gpu_lib.check_status(ws)
+    out = out.double().cpu().numpy()
+    ok = paged.visible(n, kv, True, window)
+    k, v = st.values[0][0][:, 0], st.values[1][0][:, 0]
+    s, S = sc[:, 0].astype(np.float64), float(sc.max())
+    for h in range(G):
+        qh = q[:, h].double().numpy()
+        ro, _, A = paged.attention_rows(qh, k, v, ok)
+        logit = np.where(ok, qh @ k.T / math.sqrt(d), -np.inf)
+        p = np.exp(logit - logit.max(1, keepdims=True))
+        dx = ((d + 4) * 2.0 ** -24 / math.sqrt(d) * np.where(ok, np.abs(qh) @ np.abs(k).T, 0).max(1))[:, None]
+        vmax = np.where(ok, np.abs(v).max(1), 0).max(1)[:, None]
+        tol = 2.0 ** -8 * np.abs(ro) + (3 * 2.0 ** -11 + 4 * dx + (kv + 8) * 2.0 ** -22) * A * 1.01
+        if n * G > 64:
+            tol += kv * 2.0 ** -25 * vmax + 2.0 ** -30 * S
+        else:
+            tol += (127 * np.minimum(2.0 ** -31 * S, p * s).sum(1) / p.sum(1))[:, None]
+        worst = (np.abs(out[:, h] - ro) / tol).max()
+        assert worst <= 1, f"head {h}: {worst} of the bound"
