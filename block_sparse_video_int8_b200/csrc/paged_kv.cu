@@ -3,7 +3,8 @@
 //
 // Quantiser of a (token, head) row x of d values: s = fl32(amax / 127), code = rint_half_even(fl32(x / s)),
 // 0 where s = 0: the library's block quantiser with the block shrunk to one row, so that a token can be
-// appended without touching the codes of its neighbours. Reading gives bf16(code * s).
+// appended without touching the codes of its neighbours. Reading gives bf16(code * s). A row that holds a NaN gets the
+// scale NaN and one that holds an infinity the scale inf with codes 0, so that both read back, and attend, as NaN.
 //
 // Both kernels move every byte once: writing takes 2 B in and 1 + 4/d B out an element, reading the reverse. A row of
 // d values is held by d/8 lanes (16 bytes of bf16 each), so a warp's loads and stores are whole 32-byte sectors; each
@@ -19,6 +20,20 @@ namespace {
 
 constexpr int kKvThreads = 256;
 constexpr int kWriteRows = 2;   // rows of K and of V that a thread has in flight
+
+// The larger |value| of two pairs of bf16, NaN if one is (signs of the result are meaningless), and of a pair.
+__device__ __forceinline__ uint32_t row_max(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float row_max_fold(uint32_t m) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;"
+      : "=f"(d)
+      : "f"(__uint_as_float((m & 0x7FFFu) << 16)), "f"(__uint_as_float(m & 0x7FFF0000u)));
+  return d;
+}
 
 // Codes of 8 bf16 values (w) of a row with scale sc, rcp = fl(1 / sc) or 0: the fast step of quant.cuh in pairs.
 __device__ __forceinline__ uint2 quant8(const uint32_t (&w)[4], float sc, float rcp) {
@@ -97,10 +112,10 @@ __global__ void __launch_bounds__(kKvThreads) paged_write_kernel(const PagedArgs
     float m[N];
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      uint32_t p = bmax_abs(bmax_abs(x[u].x, x[u].y), bmax_abs(x[u].z, x[u].w));
+      uint32_t p = row_max(row_max(x[u].x, x[u].y), row_max(x[u].z, x[u].w));
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) p = bmax_abs(p, __shfl_xor_sync(0xffffffffu, p, o));
-      m[u] = bmax_fold(p);
+      for (int o = LPR / 2; o > 0; o >>= 1) p = row_max(p, __shfl_xor_sync(0xffffffffu, p, o));
+      m[u] = row_max_fold(p);
     }
     // the N divisions of a row's lanes, one a lane
     static_assert(N == 4 && LPR >= 4, "four rows a thread");

@@ -438,7 +438,8 @@ size_t bsva_paged_workspace_bytes(const bsva_paged_kv* c, const bsva_paged_batch
  *   k, v       bf16 [T, H, d]; k_stride, v_stride: elements between tokens, a multiple of
  *              8 and at least H*d (a slice of a fused projection's output serves as it is)
  * Nothing is written for a sequence whose lengths break a bound, nor to a page outside
- * the cache: what the cache holds stays valid. Tokens at a negative position (kv_len
+ * the cache: what the cache holds stays valid. An INT8 row that is given a NaN or an
+ * infinity is kept as one whose values are all NaN. Tokens at a negative position (kv_len
  * smaller than the chunk) are not written and reported like a broken bound. */
 int bsva_paged_kv_write(const bsva_paged_kv* c, const bsva_paged_batch* b, const void* k, const void* v,
                         long long k_stride, long long v_stride, void* workspace,

@@ -1005,3 +1005,29 @@ def test_small_values_beside_a_large_one(gpu_lib, lens, page, window, big, d, po
             tol += (127 * np.minimum(2.0 ** -31 * S, p * s).sum(1) / p.sum(1))[:, None]
         worst = (np.abs(out[:, h] - ro) / tol).max()
         assert worst <= 1, f"head {h}: {worst} of the bound"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fill", [NAN, math.inf, -math.inf])
+def test_values_that_are_not_finite_read_back_as_nan(gpu_lib, d, fill):
+    # wherever in the row they are; the other rows are what they are without
+    st = Setup(gpu_lib, [(150, 150), (5, 40)], 2, d, 16, torch.int8, seed=d)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    want = st.cache.read(st.batch)
+    k, v = (x.clone() for x in st.new)
+    bad = torch.zeros((2, st.T, 2), dtype=torch.bool)
+    for i in range(d):
+        for z, x in enumerate((k, v)):
+            x[(i + z) % 150, i % 2, i] = fill
+            bad[z, (i + z) % 150, i % 2] = True
+    st.cache.write(k, v, st.batch)
+    got = st.cache.read(st.batch)
+    for z in range(2):
+        b = bad[z, :150].T.cuda()
+        assert torch.isnan(got[z][0, :, :150][b]).all() and torch.equal(got[z][0, :, :150][~b], want[z][0, :, :150][~b])
+        assert torch.equal(got[z][1], want[z][1])
+    for n in (1, 150):        # the last rows see every key: NaN wherever a key or value of their head is bad
+        batch = gpu_lib.PagedBatch(torch.tensor([0, n, n], dtype=torch.int32, device="cuda"), st.batch.kv_len,
+                                   st.batch.page_table, n, 150)
+        out = st.cache.attend(torch.ones((n, 2, d), dtype=torch.bfloat16, device="cuda"), batch)
+        assert torch.isnan(out[n - 1]).all()
