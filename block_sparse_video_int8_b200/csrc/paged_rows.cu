@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
   }
   // q as the B operand: lane (g, t) holds row 8 nt + g, the d values its key pieces have. With INT8 codes it enters as
   // f16, whose codes widen in fewer instructions than bf16's: a row times 2^-x with its largest value in [2^14, 2^15).
-  // That is exact but for values below 2^-29 of the row's largest, which lose at most 2^-39 of it. qf: 2^x of the
-  // rows that are this lane's columns.
+  // That is exact but for values below 2^-29 of the row's largest, which lose at most 2^-39 of it. qf: 2^x times
+  // the softmax scale, of the rows that are this lane's columns.
   uint32_t bq[NT][KS][2];
   float qf[NT][2];
 #pragma unroll
@@ -238,11 +238,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(bq[nt][kk][e] << 16)),
                                fabsf(__uint_as_float(bq[nt][kk][e] & 0xffff0000u))));
     }
-    qf[nt][0] = qf[nt][1] = 1.f;
     if constexpr (I8) {
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int x = min(max(int(__float_as_uint(top) >> 23), 15), 240) - 14;      // biased exponent of 2^x
+      const int x = min(max(int(__float_as_uint(top) >> 23), 15), 254) - 14;      // biased exponent of 2^x
       const float down = __uint_as_float(uint32_t(254 - x) << 23), up = __uint_as_float(uint32_t(x) << 23);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk)
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
           bq[nt][kk][e] = pack_f16x2(__uint_as_float(bq[nt][kk][e] << 16) * down,
                                      __uint_as_float(bq[nt][kk][e] & 0xffff0000u) * down);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) qf[nt][e] = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4);
+      for (int e = 0; e < 2; ++e) qf[nt][e] = __shfl_sync(0xffffffffu, up, (2 * t + e) * 4) * a.scale_log2;
     }
   }
 
@@ -262,13 +261,13 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     find(key + NS * STEP);
     const unsigned char* stage = ring + st * STAGE;
     uint4 kr[2][KL];
-    float ks[2] = {a.scale_log2, a.scale_log2}, vs[2];   // factors of a key's logits, INT8: scales of its values
+    float ks[2], vs[2];                   // INT8: scales of a key and of its values
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
 #pragma unroll
       for (int c = 0; c < KL; ++c) kr[e][c] = *reinterpret_cast<const uint4*>(stage + piece(kg + 8 * e, t + 4 * c));
       if constexpr (I8) {
-        ks[e] = reinterpret_cast<const float*>(stage + 32 * RB)[kg + 8 * e] * a.scale_log2;
+        ks[e] = reinterpret_cast<const float*>(stage + 32 * RB)[kg + 8 * e];
         vs[e] = reinterpret_cast<const float*>(stage + 32 * RB)[16 + kg + 8 * e];
       }
     }
@@ -297,9 +296,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_rows_kernel(const PagedArgs
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      // rounded here, not fused with the subtraction of the maximum, which was taken from rounded logits
-      x[nt][0] = __fmul_rn(x[nt][0] * qf[nt][0], ks[0]); x[nt][1] = __fmul_rn(x[nt][1] * qf[nt][1], ks[0]);
-      x[nt][2] = __fmul_rn(x[nt][2] * qf[nt][0], ks[1]); x[nt][3] = __fmul_rn(x[nt][3] * qf[nt][1], ks[1]);
+      // rounded here, not fused with the subtraction of the maximum, which was taken from rounded logits; the query's factor
+      // meets the key's first, since codes times a large query may leave fp32 where the logit does not
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[nt][e] = __fmul_rn(x[nt][e], I8 ? ks[e >> 1] * qf[nt][e & 1] : a.scale_log2);
     }
     if (key < full_lo || key + 16 > min(full_hi, hi)) {
 #pragma unroll

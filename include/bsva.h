@@ -461,7 +461,8 @@ int bsva_paged_kv_read(const bsva_paged_kv* c, const bsva_paged_batch* b, const 
  * p = kv_len - n + i; it sees key t iff t < kv_len and, when causal, t <= p and
  * (window > 0) t > p - window. A row that sees no key gets out = 0 and lse = -inf.
  *   q          bf16 [T, Hq, d]; q_stride: elements between tokens, a multiple of 8 and at
- *              least Hq*d
+ *              least Hq*d. Magnitudes below 2^118 (INT8 pages: q times codes is summed
+ *              before the scale enters)
  *   causal     0 or 1; window >= 0, 0 = none, needs causal
  *   softmax_scale  <= 0 selects 1/sqrt(d)
  *   out        out: bf16 [T, Hq, d];  lse out, nullable: fp32 [T, Hq] (natural log)

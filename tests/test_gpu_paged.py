@@ -1031,3 +1031,16 @@ def test_values_that_are_not_finite_read_back_as_nan(gpu_lib, d, fill):
                                    st.batch.page_table, n, 150)
         out = st.cache.attend(torch.ones((n, 2, d), dtype=torch.bfloat16, device="cuda"), batch)
         assert torch.isnan(out[n - 1]).all()
+
+
+@pytest.mark.parametrize("dtype,power", [(torch.int8, -100), (torch.int8, 117), (torch.bfloat16, -90), (torch.bfloat16, 90)])
+@pytest.mark.parametrize("n", [1, 5, 80])
+def test_queries_and_keys_far_from_one(gpu_lib, dtype, n, power):
+    # queries times 2^power, keys times 2^-power: the same logits. Powers of two are exact everywhere, so are the bits
+    st = Setup(gpu_lib, [(n, 300)], 2, 64, 16, dtype, seed=n, mag=0.3)
+    st.cache.write(st.new[0], st.new[1], st.batch)
+    q = st.queries(4).clamp(-0.9, 0.9).cuda()
+    want = st.cache.attend(q, st.batch, with_lse=True)
+    (st.cache.k_scale if dtype == torch.int8 else st.cache.k).mul_(2.0 ** -power)
+    got = st.cache.attend(q * 2.0 ** power, st.batch, with_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
