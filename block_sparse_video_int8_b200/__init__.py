@@ -159,13 +159,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
             f"libbsva.so not found at {path}; build it with "
             "`python -m block_sparse_video_int8_b200.build` (nvcc, sm_100a)")
     lib = ctypes.CDLL(path)
+    ver = lib.bsva_abi_version() if hasattr(lib, "bsva_abi_version") else None
+    if ver != ABI_VERSION:
+        raise RuntimeError(f"{path} has ABI version {ver}, this binding expects {ABI_VERSION}")
+    missing = [name for name in _SIGS if not hasattr(lib, name)]
+    if missing:                            # entries are added without a new version
+        raise RuntimeError(f"{path} was built from older sources: it has no {', '.join(missing)}; rebuild it with "
+                           "`python -m block_sparse_video_int8_b200.build`")
     for name, (res, args) in _SIGS.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    ver = lib.bsva_abi_version()
-    if ver != ABI_VERSION:
-        raise RuntimeError(f"{path} has ABI version {ver}, this binding expects {ABI_VERSION}")
     _LIB = lib
     return lib
 

@@ -68,7 +68,9 @@ typedef struct bsva_shape {
 } bsva_shape;
 
 /* ABI version of the loaded library; loaders compare it with BSVA_ABI_VERSION
- * ("FlashVSR Kitchen Sparse Attention", When it bites: ABI check on load). */
+ * ("FlashVSR Kitchen Sparse Attention", When it bites: ABI check on load). A version keeps
+ * every entry's arguments and meaning; entries may be added to it (the paged cache and
+ * cross attention came within version 5), so a loader that needs one looks for its symbol. */
 int bsva_abi_version(void);
 
 /* 1 if this library was built with BSVA_DEVICE_CHECKS (libbsva_checked.so), else 0.
