@@ -729,7 +729,7 @@ class PagedKVCache:
     def __init__(self, n_pages: int, page_size: int, H: int, d: int, dtype=torch.int8, device=None):
         if dtype not in (torch.int8, torch.bfloat16):
             raise TypeError(f"dtype must be torch.int8 or torch.bfloat16, got {dtype}")
-        dev = device or "cuda"
+        dev = "cuda" if device is None else device      # 0 is a device
         shape = (n_pages, H, page_size, d)
         k, v = (torch.zeros(shape, dtype=dtype, device=dev) for _ in range(2))
         ks, vs = ((torch.zeros(shape[:3], dtype=torch.float32, device=dev) for _ in range(2))

@@ -160,3 +160,16 @@ def test_binding_refuses_cpu_tensors_and_bad_types():
     x = torch.zeros((1, 2, 8, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         bsva.cross_attn_fwd(x, x, x)
+
+
+@pytest.mark.parametrize("device,want", [(None, "cuda"), (0, 0), (1, 1), ("cuda:0", "cuda:0")])
+def test_a_cache_is_allocated_on_the_device_it_is_given(monkeypatch, device, want):
+    class Seen(Exception):
+        pass
+
+    def zeros(*a, device=None, **kw):
+        raise Seen(device)
+    monkeypatch.setattr(torch, "zeros", zeros)
+    with pytest.raises(Seen) as e:
+        bsva.PagedKVCache(4, 16, 2, 64, device=device)
+    assert e.value.args == (want,)
