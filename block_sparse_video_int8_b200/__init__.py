@@ -691,7 +691,8 @@ class PagedBatch:
         for n, t in (("q_start", q_start), ("page_table", page_table)):
             if t.device != kv_len.device:
                 raise ValueError(f"{n} is on {t.device}, kv_len is on {kv_len.device}")
-        for n, x, top in (("max_q", max_q, 1 << 24), ("max_kv", max_kv, 1 << 30)):
+        for n, x, top in (("max_q", max_q, 1 << 24), ("max_kv", max_kv, 1 << 30),
+                          ("page_table's columns", page_table.shape[1], 0x7fffffff)):
             if not 1 <= x <= top:
                 raise ValueError(f"{n} = {x} outside [1, {top}]")
         self._of = (S, int(max_q), int(max_kv), q_start, kv_len, page_table)
@@ -711,6 +712,8 @@ class PagedBatch:
             raise ValueError(f"batch is on cuda:{self._index}, the call is on cuda:{index}")
         r = self._refs.get(T)
         if r is None:
+            if T > 0x7fffffff:
+                raise ValueError(f"T = {T} packed rows are past 2^31 - 1")
             if len(self._refs) >= 64:
                 self._refs.clear()
             S, max_q, max_kv, q_start, kv_len, table = self._of
@@ -833,8 +836,8 @@ class PagedKVCache:
         if stream is not None and (out is None or workspace is None or (with_lse and lse is None)):
             with _on(stream, index):
                 return self.attend(q, batch, causal, window, softmax_scale, with_lse, workspace, out, lse)
-        if window > 0x7fffffff:
-            raise ValueError(f"window = {window} is past 2^31 - 1")
+        if not -0x80000000 <= window <= 0x7fffffff:      # (the C entry refuses the other negative ones)
+            raise ValueError(f"window = {window} is no 32-bit number")
         qs = _tokens(q, None, self.d, index, "q")
         T, Hq, d = q.shape
         b = batch._ref(T, index)

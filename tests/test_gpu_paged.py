@@ -1044,3 +1044,18 @@ def test_queries_and_keys_far_from_one(gpu_lib, dtype, n, power):
     (st.cache.k_scale if dtype == torch.int8 else st.cache.k).mul_(2.0 ** -power)
     got = st.cache.attend(q * 2.0 ** power, st.batch, with_lse=True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_numbers_past_32_bits_are_refused(gpu_lib):
+    # nothing wraps on its way into the C entries
+    st = Setup(gpu_lib, [(1, 20)] * 130, 2, 64, 16, torch.int8, seed=5)
+    b, q = st.batch, st.queries(4).cuda()
+    for window in (-2 ** 31 - 1, -2 ** 32 + 5, 2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError, match="window"):
+            st.cache.attend(q, b, window=window)
+    loose = gpu_lib.PagedBatch(b.q_start, b.kv_len, b.page_table, 2 ** 24, 20)
+    with pytest.raises(ValueError, match="packed rows"):     # the default, S * max_q, is 130 * 2^24
+        st.cache.new_workspace(loose, 4)
+    ws = st.cache.new_workspace(loose, 4, st.T)
+    st.cache.write(st.new[0], st.new[1], loose, workspace=ws)
+    gpu_lib.check_status(ws)
