@@ -29,11 +29,12 @@
 // outweighs the others cancels, and the log-sum-exp takes the sum of the unrounded ones (LSE). f16 weights round eight
 // times finer and need neither.
 // Measured, heads of 128 (floor: 4 flops a row, key and d value at 1634 TFLOP/s): 1536 new of 12288 tokens, 12 heads,
-// bf16 pages 129 us, 143 with the log-sum-exp (floor 66); tensor and exponential pipes 48 % busy, issue slots 35 %: a
+// bf16 pages 129 us, 140 with the log-sum-exp (floor 66); tensor and exponential pipes 48 % busy, issue slots 35 %: a
 // half waits for its own chain, weights - product - next logits, which P over S leaves in a row. 32760 x 512 tokens,
-// 40 heads, contiguous: 390 us (floor 210), a quarter of it each item's output and start. 2048 of 32760 tokens, 40
-// query and 8 key heads, INT8 pages: 2054 us (floor 815); the loaders' widening takes shared memory (44 %) and issue
-// slots (39 %) from the softmax.
+// 40 heads, contiguous: 390 us after a pause, 434 back to back (floor 210), a quarter of it each item's output and start.
+// 2048 of 32760 tokens, 40 query and 8 key heads, INT8 pages: 2100 us (floor 815); the loaders widen every key once an
+// item, which takes shared memory (44 %) and issue slots (38 %) from the softmax. No pipe is full in any of the three:
+// these are costs of this arrangement, not bounds of the operators.
 // Every wait is bounded as in attn_sm100.cu.
 #include "paged.cuh"
 
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kTileThreads<I8>, 1)
   };
 
   // Registers go to the softmax. INT8, 512 threads with 128 each: 2 x 168 + 64 + 112 = 4 x 128 for the four warpgroups
-  // (2048 x 32760 tokens, us: 2054; 56 and 120 for the last two 2070; 2 x 176 + 56 + 104 2079; 2 x 160 + 72 + 120 2130).
+  // (2048 x 32760 tokens, us: 2100; 56 and 120 for the last two 2096; 2 x 176 + 56 + 104 2102; 2 x 160 + 72 + 120 2170).
   // bf16, 384 threads with 168 each: 2 x 184 + 136 = 2 x 192 + 120 = 3 x 168, with which nothing is spilled. (A fourth
   // warpgroup for the output leaves the others too few: 32760 x 512 tokens, 40 heads, 446 us for 393.)
   if (warp < 8) {
