@@ -424,7 +424,7 @@ typedef struct bsva_paged_kv {
  * invalid. Rows of packed outputs outside [q_start[0], q_start[S]) are left as they were. */
 typedef struct bsva_paged_batch {
   int S, T;                   /* sequences; rows of the packed tensors                  */
-  int max_q, max_kv;          /* bounds, max_q >= 1, max_kv >= 1                        */
+  int max_q, max_kv;          /* bounds, max_q in [1, 2^24], max_kv in [1, 2^30]         */
   int max_pages;              /* columns of page_table, max_kv <= max_pages*page_size   */
   const int32_t* q_start;     /* device int32 [S+1], ascending                          */
   const int32_t* kv_len;      /* device int32 [S]                                       */
@@ -438,7 +438,8 @@ size_t bsva_paged_workspace_bytes(const bsva_paged_kv* c, const bsva_paged_batch
 
 /* Writes the batch's new tokens into their pages (quantised for BSVA_KV_INT8).
  *   k, v       bf16 [T, H, d]; k_stride, v_stride: elements between tokens, a multiple of
- *              8 and at least H*d (a slice of a fused projection's output serves as it is)
+ *              8 and at least H*d (a slice of a fused projection's output serves as it is).
+ *              max_q * H is at most 2^30
  * Nothing is written for a sequence whose lengths break a bound, nor to a page outside
  * the cache: what the cache holds stays valid. An INT8 row that is given a NaN or an
  * infinity is kept as one whose values are all NaN. Tokens at a negative position (kv_len
@@ -453,7 +454,7 @@ int bsva_paged_kv_write(const bsva_paged_kv* c, const bsva_paged_batch* b, const
  *   first      device int32 [S], NULL = 0; a start behind the end gives zeros
  *   L          rows per sequence, >= 1; kv_len[s] - first[s] <= L
  *   k_out, v_out  out: bf16 [S, H, L, d]
- * q_start is not used and may be NULL; T and max_q are not used. */
+ * q_start is not used and may be NULL; T and max_q only have to be in their ranges. */
 int bsva_paged_kv_read(const bsva_paged_kv* c, const bsva_paged_batch* b, const int32_t* first, int L,
                        void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
                        bsva_stream_t stream);
@@ -464,7 +465,7 @@ int bsva_paged_kv_read(const bsva_paged_kv* c, const bsva_paged_batch* b, const 
  * (window > 0) t > p - window. A row that sees no key gets out = 0 and lse = -inf.
  *   q          bf16 [T, Hq, d]; q_stride: elements between tokens, a multiple of 8 and at
  *              least Hq*d. Magnitudes below 2^118 (INT8 pages: q times codes is summed
- *              before the scale enters)
+ *              before the scale enters). max_q * Hq / H is at most 2^30
  *   causal     0 or 1; window >= 0, 0 = none, needs causal
  *   softmax_scale  <= 0 selects 1/sqrt(d)
  *   out        out: bf16 [T, Hq, d];  lse out, nullable: fp32 [T, Hq] (natural log)

@@ -5,7 +5,7 @@ the output's rounding 2^-8 |o|; the roundings before the second product:
  - INT8 values, f16: a weight, a scale and a value times its scale are rounded once each, 3 2^-11 A. What is below
    2^-14 loses up to 2^-25 instead: a weight that of the largest value, n 2^-24 max|v| for n of them; a value, which
    enters as code * (s c) / 4096 with s c >= 1 for the largest scale s, 2^-25 4096 s <= 2^-13 max|v| / 127 < 2^-19 max|v|,
-   times weights that sum to 1.
+   times weights that sum to 1. (Values enter as code * (s c) with s c >= 2^5 for the largest scale, which loses less.)
  - bf16 values: a weight p enters as p (1 + e), |e| <= 2^-8, and the sum that divides as it entered, so that o moves by
    sum p e (v - o) / sum p (1 + e), at most 2^-8 (A + |o|) (1 + 2^-7).
 A logit x of d products in fp32 is off by dx = (d + 4) 2^-24 scale sum|q||k|, which moves a weight by
